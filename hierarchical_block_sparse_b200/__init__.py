@@ -12,6 +12,9 @@ from .pisa import (  # noqa: F401
     pisa_build_pyramid_prefix, pisa_pyramid_append, pisa_decode, pisa_status_string, pisa_version,
     pisa_workspace_bytes, pisa_select_ws, pisa_sparse_attn_ws, pisa_forward_ws, alloc_workspace,
     pisa_workspace_status,
+    PisaPages, make_pages, pages_width, pisa_pages_state_words, pisa_pages_init, pisa_pages_reserve, pisa_pages_fork,
+    pisa_pages_free, pisa_pages_compact, pisa_pages_copy, pisa_paged_append, pisa_paged_workspace_bytes,
+    alloc_paged_workspace, pisa_paged_attn, pisa_paged_build_pyramid, pisa_paged_decode_step, PagedCache,
 )
 
 __version__ = "0.1.0"

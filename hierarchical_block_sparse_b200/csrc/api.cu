@@ -139,6 +139,8 @@ DecodeParams decode_params(const pisa_cfg* c, const Geom& g) {
 
 }  // namespace
 
+int pisa::check_gpu_cfg(const pisa_cfg* c) { return check_gpu(c); }
+
 extern "C" {
 
 int pisa_num_levels(const pisa_cfg* cfg) {

@@ -11,6 +11,10 @@
 // per level), all warps then split the leaf scoring (exact LSE over raw keys)
 // and, after warp 0's final Top-K, the attention over the kept blocks;
 // partial softmax states are merged through shared memory.
+//
+// The same kernel serves the paged cache (PAGED): a page holds whole leaves, so
+// a leaf's rows stay one run of memory and only its first row is looked up,
+// once, when the leaf enters the list; everything downstream is unchanged.
 #include "pisa_internal.h"
 #include "pisa_walk.cuh"
 #include "tc.cuh"
@@ -24,12 +28,13 @@ __device__ __forceinline__ void bar_sync(int id, int count) {
 
 // Summaries' update of one (b, kv-head) for the row at n: NWA warps (wi =
 // this warp's index among them) write the new key/value row, fetch the leaf's
-// cached rows before n (summed per warp, INFLIGHT loads in flight per lane)
+// cached rows before n (Kl, Vl: the leaf's first rows; summed per warp,
+// INFLIGHT loads in flight per lane)
 // and the sibling of each ancestor into `scratch` ((NWA + kMaxLevels) x D
 // floats of shared memory) -- none of which depends on the new row -- meet on
 // named barrier `bar`, and warp 0 of them runs the chain leaf -> root.
 template <typename T, int D, int NWA>
-__device__ __forceinline__ void append_unit(T* Kh, T* Vh, float* P, const T* krow, const T* vrow, int64_t n,
+__device__ __forceinline__ void append_unit(T* Kl, T* Vl, float* P, const T* krow, const T* vrow, int64_t n,
                                             const DecodeParams& p, int wi, int lane, float* scratch, int bar) {
     constexpr int VD = D / 32;
     constexpr int INFLIGHT = 8;
@@ -37,13 +42,13 @@ __device__ __forceinline__ void append_unit(T* Kh, T* Vh, float* P, const T* kro
     float* s_sib = scratch + NWA * D;   // [kMaxLevels][D]
     float kn[VD];
     Ld<T, VD>::run(krow + lane * VD, kn);
+    const int64_t leaf = n / p.C, lo = leaf * p.C;
     if (wi == 0) {
         float vn[VD];
         Ld<T, VD>::run(vrow + lane * VD, vn);
-        store_vec<T, VD>(Kh + n * D + lane * VD, kn);
-        store_vec<T, VD>(Vh + n * D + lane * VD, vn);
+        store_vec<T, VD>(Kl + (n - lo) * D + lane * VD, kn);
+        store_vec<T, VD>(Vl + (n - lo) * D + lane * VD, vn);
     }
-    const int64_t leaf = n / p.C, lo = leaf * p.C;
     float acc[VD];
 #pragma unroll
     for (int e = 0; e < VD; ++e) acc[e] = 0.f;
@@ -53,7 +58,7 @@ __device__ __forceinline__ void append_unit(T* Kh, T* Vh, float* P, const T* kro
         for (int i = 0; i < INFLIGHT; ++i) {
             const int64_t r = r0 + (int64_t)i * NWA;
             if (r < n) {
-                Ld<T, VD>::run(Kh + r * D + lane * VD, x[i]);
+                Ld<T, VD>::run(Kl + (r - lo) * D + lane * VD, x[i]);
             } else {
 #pragma unroll
                 for (int e = 0; e < VD; ++e) x[i][e] = 0.f;
@@ -112,7 +117,8 @@ __global__ void __launch_bounds__(128) append_kernel(T* __restrict__ Kc, T* __re
     const int64_t b = unit / p.Hkv;
     const int64_t n = pos[b];
     if (n < 0 || n >= p.N) return;
-    append_unit<T, D, 4>(Kc + unit * p.N * D, Vc + unit * p.N * D, pyr + unit * p.geom.rows * D, k_new + unit * D,
+    const int64_t row = unit * p.N + n / p.C * p.C;  // the leaf's first
+    append_unit<T, D, 4>(Kc + row * D, Vc + row * D, pyr + unit * p.geom.rows * D, k_new + unit * D,
                          v_new + unit * D, n, p, threadIdx.x >> 5, threadIdx.x & 31, scratch, 0);
 }
 
@@ -203,7 +209,8 @@ constexpr bool decode_caches() { return G == 1; }
 template <int G>
 constexpr int decode_stages() { return decode_caches<G>() ? 2 : 3; }
 
-template <typename T, int D, int G>
+// PAGED: Kc, Vc are the pools [P, Hkv, S, D] and `pos` holds the lengths, the new token included.
+template <typename T, int D, int G, bool PAGED>
 __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
     const T* __restrict__ q_new, T* __restrict__ Kc, T* __restrict__ Vc, float* __restrict__ pyr,
     const int32_t* __restrict__ pos, int32_t* __restrict__ idx, T* __restrict__ out, const T* __restrict__ k_new,
@@ -235,18 +242,27 @@ __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
     float* s_logit = reinterpret_cast<float*>(dsm + kDecStages * kDecStageBytes + 5 * sizeof(Part));
     const bool cached = decode_caches<G>() && p.C <= kDecCacheKeys;
     __shared__ int s_kj[32];  // for each kept leaf, its index in the scored list
+    __shared__ int s_row[PAGED ? 32 : 1];  // the pool row at which each listed leaf begins (-1: it has no page)
     const int64_t unit = blockIdx.x;  // b * Hkv + kvh
     const int64_t b = unit / p.Hkv;
     const int kvh = (int)(unit - b * p.Hkv);
-    const int64_t t = pos[b];
-    if (t < 0 || t >= p.N) {
+    const int64_t t = PAGED ? (int64_t)pos[b] - 1 : pos[b];
+    // first pool row of a leaf (pages hold whole leaves; the pool has < 2^31 rows)
+    auto leaf_row = [&](int64_t leaf) -> int {
+        const int tok = (int)leaf * p.C;
+        const int page = __ldg(p.table + b * p.W + tok / p.S);
+        return (unsigned)page < (unsigned)p.P ? (page * p.Hkv + kvh) * p.S + tok % p.S : -1;
+    };
+    int new_row = 0;  // PAGED: of the new token's leaf
+    if (PAGED && t >= 0 && t < p.N) new_row = leaf_row(t / p.C);
+    if (t < 0 || t >= p.N || new_row < 0) {
         if (tid < p.K) idx[unit * p.K + tid] = -1;
         for (int i = tid; i < G * D; i += blockDim.x) out[((b * p.Hq + (int64_t)kvh * G) * D) + i] = (T)0.f;
         return;
     }
     const int64_t n_keys = t + 1;
-    const T* Kh = Kc + unit * p.N * D;
-    const T* Vh = Vc + unit * p.N * D;
+    const T* Kh = PAGED ? Kc : Kc + unit * p.N * D;
+    const T* Vh = PAGED ? Vc : Vc + unit * p.N * D;
     const float* P = pyr + unit * p.geom.rows * D;
     const Forced F(t, p.C, 1, p.forced_mask);
     for (int i = tid; i < G * D; i += blockDim.x) {
@@ -260,10 +276,11 @@ __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
     // those rows: they are the forced path (never scored), and the parent of
     // an ancestor is an ancestor. The new key/value row is read back only by
     // the attention, after later barriers.
-    if (k_new != nullptr && warp >= 1)
-        append_unit<T, D, NW - 1>(Kc + unit * p.N * D, Vc + unit * p.N * D, pyr + unit * p.geom.rows * D,
-                                  k_new + unit * D, v_new + unit * D, t, p, warp - 1, lane,
-                                  reinterpret_cast<float*>(dsm), 1);
+    if (k_new != nullptr && warp >= 1) {
+        const int64_t row = PAGED ? (int64_t)new_row : unit * p.N + t / p.C * p.C;
+        append_unit<T, D, NW - 1>(Kc + row * D, Vc + row * D, pyr + unit * p.geom.rows * D, k_new + unit * D,
+                                  v_new + unit * D, t, p, warp - 1, lane, reinterpret_cast<float*>(dsm), 1);
+    }
 
     // ---- internal levels. Warp 0 carries the walk (lane c = candidate c,
     // valid candidates in ascending node order) and passes alone through the
@@ -369,6 +386,7 @@ __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
             const int j = __popc(s.vmask & ((1u << lane) - 1u));
             s_sel[j] = cand;
             s_slot[j] = lane;
+            if constexpr (PAGED) s_row[j] = leaf_row(cand);
         }
         if (lane == 0) s_nlist = s.n;
     }
@@ -380,7 +398,13 @@ __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
         auto rows_of = [&](int tile, int64_t& lo) {
             const int64_t leaf = s_sel[tile / tpl];
             lo = leaf * p.C + (int64_t)(tile % tpl) * Lo::RowsB;
-            return (int)(min(min(leaf * p.C + p.C, n_keys), lo + Lo::RowsB) - lo);
+            const int n = (int)(min(min(leaf * p.C + p.C, n_keys), lo + Lo::RowsB) - lo);
+            if constexpr (PAGED) {  // lo: the row of the pool
+                const int row = s_row[tile / tpl];
+                lo = row + (tile % tpl) * Lo::RowsB;
+                return row < 0 ? 0 : n;
+            }
+            return n;
         };
         auto issue = [&](int tile) {
             if (tile < ntiles) {
@@ -513,6 +537,7 @@ __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
         if ((kmask >> lane) & 1u)  // kept candidate lane -> (its rank among the kept, among the scored)
             s_kj[__popc(kmask & ((1u << lane) - 1u))] = __popc(s.vmask & ((1u << lane) - 1u));
         s_sel[lane] = lane < p.K ? out_id : -1;
+        if constexpr (PAGED) s_row[lane] = lane < p.K && out_id >= 0 ? leaf_row(out_id) : -1;
         if (lane == 0) s_nlist = min(kept, p.K);
 #pragma unroll
         for (int h = 0; h < G; ++h) {
@@ -549,7 +574,13 @@ __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
             const int64_t blk = s_sel[tile / tpl];
             lo = blk * p.C + (int64_t)(tile % tpl) * Lo::RowsC;
             const int64_t hi = min(min(blk * p.C + p.C, n_keys), lo + Lo::RowsC);
-            return (int)max(hi - lo, (int64_t)0);
+            const int n = (int)max(hi - lo, (int64_t)0);
+            if constexpr (PAGED) {
+                const int row = s_row[tile / tpl];
+                lo = row + (tile % tpl) * Lo::RowsC;
+                return row < 0 ? 0 : n;
+            }
+            return n;
         };
         auto issue = [&](int tile) {
             if (tile < ntiles) {
@@ -673,8 +704,8 @@ cudaError_t launch_append(int dtype, int d, void* Kc, void* Vc, float* pyr, cons
     return cudaErrorInvalidValue;
 }
 
-template <typename T, int D, int G>
-static cudaError_t launch_decode_t(const void* q, void* Kc, void* Vc, float* pyr, const int32_t* pos, int32_t* idx,
+template <typename T, int D, int G, bool PAGED>
+static cudaError_t launch_decode_p(const void* q, void* Kc, void* Vc, float* pyr, const int32_t* pos, int32_t* idx,
                                    void* o, const void* k_new, const void* v_new, const DecodeParams& p,
                                    cudaStream_t st) {
     const size_t out_bytes = sizeof(float) * 8 * G * (D + 1);
@@ -682,7 +713,7 @@ static cudaError_t launch_decode_t(const void* q, void* Kc, void* Vc, float* pyr
     const size_t stage_bytes = (size_t)decode_stages<G>() * kDecStageBytes + 5 * sizeof(float) * 32 * 8 * G +
                                (decode_caches<G>() ? sizeof(float) * 32 * kDecCacheKeys : 0);
     const size_t smem = out_bytes > stage_bytes ? out_bytes : stage_bytes;
-    auto kern = decode_kernel<T, D, G>;
+    auto kern = decode_kernel<T, D, G, PAGED>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     // the pipeline stages of decode_min_blocks<G>() CTAs must fit in one SM's shared memory
@@ -691,6 +722,14 @@ static cudaError_t launch_decode_t(const void* q, void* Kc, void* Vc, float* pyr
     kern<<<(unsigned)((int64_t)p.B * p.Hkv), 256, smem, st>>>((const T*)q, (T*)Kc, (T*)Vc, pyr, pos, idx, (T*)o,
                                                                (const T*)k_new, (const T*)v_new, p);
     return cudaGetLastError();
+}
+
+template <typename T, int D, int G>
+static cudaError_t launch_decode_t(const void* q, void* Kc, void* Vc, float* pyr, const int32_t* pos, int32_t* idx,
+                                   void* o, const void* k_new, const void* v_new, const DecodeParams& p,
+                                   cudaStream_t st) {
+    return p.table ? launch_decode_p<T, D, G, true>(q, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st)
+                   : launch_decode_p<T, D, G, false>(q, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
 }
 
 template <typename T, int D>
@@ -708,7 +747,8 @@ static cudaError_t launch_decode_d(const void* q, void* Kc, void* Vc, float* pyr
 }
 
 // k_new / v_new null: decode only (the row at pos was appended before);
-// otherwise the append runs inside the same kernel.
+// otherwise the append runs inside the same kernel. With p.table, Kc and Vc are
+// the pools of a paged cache and pos holds the lengths, the new token included.
 cudaError_t launch_decode(int dtype, int d, const void* q_new, void* Kc, void* Vc, float* pyr, const int32_t* pos,
                           int32_t* idx, void* o, const void* k_new, const void* v_new, const DecodeParams& p,
                           cudaStream_t st) {

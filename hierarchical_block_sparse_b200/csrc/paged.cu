@@ -1,0 +1,767 @@
+// paged.cu -- attention of one new token a sequence over a paged cache.
+//
+//   z_j = q . k_j / sqrt(d) over the len[b] cached keys;  o = sum_j e^(z_j) v_j / sum_j e^(z_j)
+//
+// One pass over the keys and values with a running maximum and sum (in log2
+// units). The work is a list of tiles of TK keys, ordered by (sequence, KV
+// head, position); CTA c of `grid` takes the c-th equal share of that list,
+// whatever the lengths, so one long sequence and many short ones load the
+// GPU alike. A (sequence, KV head) unit that falls into one share is finished
+// by its CTA; one that is cut leaves (max, sum, unnormalised o) of each part in
+// the workspace, which paged_join_kernel joins in share order (the result
+// depends on the lengths alone, not on timing).
+//
+// Inside a CTA each of the 4 warps takes KT keys of a tile and streams them
+// through a ring of its own (cp.async, kStages x 8 KB), with no barrier
+// before the unit ends: a warp that waits for memory holds up no other.
+#include "pisa_internal.h"
+#include "pisa_paged.cuh"
+#include "tc.cuh"
+
+namespace pisa {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kStages = 3;
+constexpr int kStageBytes = 8192;  // KT key rows, then KT value rows
+constexpr float kRescale = 8.f;    // see softmax below
+constexpr float kTiny = 1.17549435e-38f;  // smallest normal number
+
+__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool live) {
+    const int bytes = live ? 16 : 0;  // 0: the 16 bytes become zeros, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), bf16
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// byte offset of 16-byte chunk c of row r: chunks are XOR-swizzled by the row
+// so that the 8 rows of one ldmatrix phase hit distinct banks
+template <int RowBytes>
+__device__ __forceinline__ uint32_t ring_off(int r, int c) {
+    return (uint32_t)(r * RowBytes + ((c ^ (r & 7)) << 4));
+}
+
+// ---- one warp's tile, bf16: tensor cores -------------------------------------------
+//
+// S = Q K^T and O += P V as m16n8k16 products whose 16 rows are the group's
+// query heads. Decode needs 4 G products a key element pair against 4 bytes of
+// it, far below what even these instructions do per byte of HBM traffic, so the
+// shapes are chosen for short latency and few registers. P enters as bf16 high
+// and low parts (2^-16 relative): in one rounding its error would be as large as
+// the output's own. The high part is cut, not rounded, and the low part is kept
+// above zero, so that an infinite value times both stays that infinity. With
+// G <= 8 the low parts ride in the tile's unused rows 8..15 and cost nothing;
+// G = 16 takes a second product.
+template <int D_, int G_>
+struct MmaTile {
+    using T = __nv_bfloat16;
+    static constexpr int D = D_, G = G_;
+    static constexpr int KT = kStageBytes / (2 * D * 2);  // 16 (d = 128) or 32 (d = 64) keys
+    static constexpr int RowBytes = D * 2;
+    static constexpr int kScratchFloats = 0;
+    static constexpr int RB = G > 8 ? 2 : 1;  // accumulator row blocks that hold heads
+
+    uint32_t qa[D / 16][4];
+    float o[D / 8][4];
+    float m[RB], l[RB];
+
+    __device__ __forceinline__ void load_q(const T* q, float, int lane) {
+        const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int h = g + (i & 1) * 8, e = k * 16 + 2 * c + (i >> 1) * 8;
+                qa[k][i] = h < G ? __ldg(reinterpret_cast<const unsigned*>(q + (size_t)h * D + e)) : 0u;
+            }
+    }
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+        }
+    }
+    // keys of this tile whose bit is set in `mask` count
+    __device__ __forceinline__ void step(uint32_t kbuf, uint32_t vbuf, unsigned mask, float qscale, int lane, float*) {
+        const int c = lane & 3;
+        float s[KT / 8][4];
+#pragma unroll
+        for (int j = 0; j < KT / 8; ++j) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[j][i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                uint32_t b[4];
+                ldsm4(kbuf + ring_off<RowBytes>(8 * j + (lane & 7), 4 * k + (lane >> 3)), b);
+                mma16816(s[j], qa[2 * k], b[0], b[1]);
+                mma16816(s[j], qa[2 * k + 1], b[2], b[3]);
+            }
+        }
+        // Running maximum: it is only moved when a logit passes it by more than
+        // kRescale (the terms then stay below 2^8, far from overflow), so most tiles
+        // skip the rescaling of o.
+        float mx[RB];
+        bool move = false;
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+            mx[i] = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < KT / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const bool live = (mask >> (8 * j + 2 * c + e)) & 1u;
+                    s[j][2 * i + e] = live ? s[j][2 * i + e] * qscale : -INFINITY;
+                    mx[i] = fmaxf(mx[i], s[j][2 * i + e]);
+                }
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 2));
+            move |= mx[i] > m[i] + kRescale;
+        }
+        if (__any_sync(kFull, move)) {
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                const float mn = fmaxf(m[i], mx[i]);
+                const float a = mn == -INFINITY ? 1.f : exp2f(m[i] - mn);
+                m[i] = mn;
+                l[i] *= a;
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) {
+                    o[j][2 * i] *= a;
+                    o[j][2 * i + 1] *= a;
+                    if (RB == 1) {  // the low parts' rows belong to the same head
+                        o[j][2] *= a;
+                        o[j][3] *= a;
+                    }
+                }
+            }
+        }
+        uint32_t hi[KT / 8][2], lo[KT / 8][2];  // P: column pair of row block 0 and 1
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+            const float mu = m[i] == -INFINITY ? 0.f : m[i];
+#pragma unroll
+            for (int j = 0; j < KT / 8; ++j) {
+                const float p0 = ex2_approx(s[j][2 * i] - mu), p1 = ex2_approx(s[j][2 * i + 1] - mu);
+                l[i] += p0 + p1;
+                const unsigned u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+                hi[j][i] = __byte_perm(u0, u1, 0x7632);
+                lo[j][i] = pack_bf16(fmaxf(p0 - __uint_as_float(u0 & 0xffff0000u), kTiny),
+                                     fmaxf(p1 - __uint_as_float(u1 & 0xffff0000u), kTiny));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < KT / 16; ++k) {
+            uint32_t pa[4], pl[4];
+            if constexpr (RB == 1) {
+                pa[0] = hi[2 * k][0];
+                pa[1] = lo[2 * k][0];
+                pa[2] = hi[2 * k + 1][0];
+                pa[3] = lo[2 * k + 1][0];
+            } else {
+                pa[0] = hi[2 * k][0];
+                pa[1] = hi[2 * k][1];
+                pa[2] = hi[2 * k + 1][0];
+                pa[3] = hi[2 * k + 1][1];
+                pl[0] = lo[2 * k][0];
+                pl[1] = lo[2 * k][1];
+                pl[2] = lo[2 * k + 1][0];
+                pl[3] = lo[2 * k + 1][1];
+            }
+            const int key = 16 * k + ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                uint32_t b[4];
+                ldsm4_t(vbuf + ring_off<RowBytes>(key, 2 * j + (lane >> 4)), b);
+                mma16816(o[2 * j], pa, b[0], b[1]);
+                mma16816(o[2 * j + 1], pa, b[2], b[3]);
+                if constexpr (RB == 2) {
+                    mma16816(o[2 * j], pl, b[0], b[1]);
+                    mma16816(o[2 * j + 1], pl, b[2], b[3]);
+                }
+            }
+        }
+    }
+    // this warp's state into a merge slot ([G][D] o, then m[G], l[G]); `add`: merged with what is there
+    __device__ __forceinline__ void put(float* slot, bool add, int lane) {
+        const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+            float sum = l[i];
+            sum += __shfl_xor_sync(kFull, sum, 1);
+            sum += __shfl_xor_sync(kFull, sum, 2);
+            const int h = g + 8 * i;
+            float a = 1.f, b = 0.f, mn = m[i];
+            if (add && h < G) {
+                const float ms = slot[G * D + h];
+                mn = fmaxf(m[i], ms);
+                a = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mn);
+                b = ms == -INFINITY ? 0.f : exp2f(ms - mn);
+                sum = a * sum + b * slot[G * D + G + h];
+            }
+            __syncwarp();
+            if (h < G) {
+                if (c == 0) {
+                    slot[G * D + h] = mn;
+                    slot[G * D + G + h] = sum;
+                }
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) {
+                    float x0 = o[j][2 * i], x1 = o[j][2 * i + 1];
+                    if (RB == 1) {
+                        x0 += o[j][2];
+                        x1 += o[j][3];
+                    }
+                    float* p = slot + h * D + 8 * j + 2 * c;
+                    p[0] = add ? a * x0 + b * p[0] : x0;
+                    p[1] = add ? a * x1 + b * p[1] : x1;
+                }
+            }
+        }
+    }
+};
+
+// ---- one warp's tile, fp32: CUDA cores -----------------------------------------------
+//
+// A lane owns 4 dims of a row (D / 4 lanes a row, 32 * 4 / D rows at a time);
+// the G partial dots of several rows are summed across lanes in one
+// reduce-scatter, and the probabilities come back through shared memory.
+template <int D_, int G_>
+struct FmaTile {
+    using T = float;
+    static constexpr int D = D_, G = G_;
+    static constexpr int KT = kStageBytes / (2 * D * 4);  // 8 (d = 128) or 16 (d = 64) keys
+    static constexpr int RowBytes = D * 4;
+    static constexpr int LR = D / 4;       // lanes a row
+    static constexpr int RP = 32 / LR;     // rows at a time
+    static constexpr int RI = KT / RP;     // rows a lane takes part in
+    static constexpr int kScratchFloats = KT * G + G;
+    static constexpr int NB = RI * G < LR ? RI * G : LR;  // values of one reduce-scatter
+
+    float q[G][4], o[G][4];
+    float m, l;  // of head lane % G (G <= 16 lanes hold it several times over; l is a share)
+
+    __device__ __forceinline__ void load_q(const T* src, float qscale, int lane) {
+        const int e = (lane % LR) * 4;
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(src + (size_t)h * D + e));
+            q[h][0] = v.x * qscale;
+            q[h][1] = v.y * qscale;
+            q[h][2] = v.z * qscale;
+            q[h][3] = v.w * qscale;
+        }
+    }
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int h = 0; h < G; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[h][e] = 0.f;
+        m = -INFINITY;
+        l = 0.f;
+    }
+    static __device__ __forceinline__ float4 row16(uint32_t buf, int r, int c) {
+        float4 v;
+        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];\n"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(buf + ring_off<RowBytes>(r, c))
+                     : "memory");
+        return v;
+    }
+    __device__ __forceinline__ void step(uint32_t kbuf, uint32_t vbuf, unsigned mask, float, int lane, float* scratch) {
+        const int sub = lane / LR, c = lane % LR;
+        constexpr int RowsB = NB / G;  // rows (of this lane's) in one reduce-scatter
+#pragma unroll
+        for (int r0 = 0; r0 < RI; r0 += RowsB) {
+            float v[NB];
+#pragma unroll
+            for (int r = 0; r < RowsB; ++r) {
+                const float4 x = row16(kbuf, (r0 + r) * RP + sub, c);
+#pragma unroll
+                for (int h = 0; h < G; ++h)
+                    v[r * G + h] = fmaf(q[h][0], x.x, fmaf(q[h][1], x.y, fmaf(q[h][2], x.z, q[h][3] * x.w)));
+            }
+            int n = NB;
+#pragma unroll
+            for (int w = LR / 2; w >= 1; w >>= 1) {
+                if (n > 1) {
+                    n >>= 1;
+                    const bool hi = (lane & w) != 0;
+#pragma unroll
+                    for (int i = 0; i < NB / 2; ++i)
+                        if (i < n) {
+                            const float send = hi ? v[i] : v[i + n], keep = hi ? v[i + n] : v[i];
+                            v[i] = keep + __shfl_xor_sync(kFull, send, w);
+                        }
+                } else {
+                    v[0] += __shfl_xor_sync(kFull, v[0], w);
+                }
+            }
+            const int i = (lane % LR) / (LR / NB);  // the value this lane ended with
+            scratch[((r0 + i / G) * RP + sub) * G + i % G] = v[0];
+        }
+        __syncwarp();
+        // head h = lane % G, keys lane / G, lane / G + 32 / G, ...
+        constexpr int PER = (KT * G + 31) / 32;
+        const int h = lane % G;
+        float z[PER], mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int key = lane / G + i * (32 / G);
+            z[i] = key < KT && ((mask >> key) & 1u) ? scratch[key * G + h] : -INFINITY;
+            mx = fmaxf(mx, z[i]);
+        }
+#pragma unroll
+        for (int w = G; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, w));
+        const bool move = __any_sync(kFull, mx > m + kRescale);
+        if (move) {
+            const float mn = fmaxf(m, mx);
+            const float a = mn == -INFINITY ? 1.f : exp2f(m - mn);
+            m = mn;
+            l *= a;
+            if (lane < G) scratch[KT * G + lane] = a;
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int key = lane / G + i * (32 / G);
+            if (key < KT) {
+                const float p = exp2f(z[i] - mu);
+                l += p;
+                scratch[key * G + h] = p;
+            }
+        }
+        __syncwarp();
+        if (move) {
+#pragma unroll
+            for (int hh = 0; hh < G; ++hh) {
+                const float a = scratch[KT * G + hh];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[hh][e] *= a;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < RI; ++r) {
+            const int key = r * RP + sub;
+            const float4 x = row16(vbuf, key, c);
+#pragma unroll
+            for (int hh = 0; hh < G; ++hh) {
+                const float p = scratch[key * G + hh];
+                o[hh][0] = fmaf(p, x.x, o[hh][0]);
+                o[hh][1] = fmaf(p, x.y, o[hh][1]);
+                o[hh][2] = fmaf(p, x.z, o[hh][2]);
+                o[hh][3] = fmaf(p, x.w, o[hh][3]);
+            }
+        }
+        __syncwarp();  // scratch is rewritten by the next tile
+    }
+    __device__ __forceinline__ void put(float* slot, bool add, int lane) {
+        float sum = l;
+#pragma unroll
+        for (int w = G; w < 32; w <<= 1) sum += __shfl_xor_sync(kFull, sum, w);
+        float a = 1.f, b = 0.f, mn = m;
+        if (add) {
+            const float ms = slot[G * D + lane % G];
+            mn = fmaxf(m, ms);
+            a = m == -INFINITY ? 0.f : exp2f(m - mn);
+            b = ms == -INFINITY ? 0.f : exp2f(ms - mn);
+            sum = a * sum + b * slot[G * D + G + lane % G];
+        }
+        __syncwarp();
+        if (lane < G) {
+            slot[G * D + lane] = mn;
+            slot[G * D + G + lane] = sum;
+        }
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+            const float ah = __shfl_sync(kFull, a, h), bh = __shfl_sync(kFull, b, h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float x = o[h][e];
+                if (RP == 2) x += __shfl_xor_sync(kFull, x, LR);  // the two rows' shares of a dim
+                float* p = slot + h * D + (lane % LR) * 4 + e;
+                if (lane < LR) *p = add ? ah * x + bh * *p : x;
+            }
+        }
+    }
+};
+
+// ---- the list of tiles ------------------------------------------------------------------
+
+struct Share {
+    int64_t unit0;     // first tile of the unit at x (in the list)
+    int b, h, t;       // sequence (-1: none), KV head and tile inside the unit at x
+    int n, nt;         // keys and tiles of sequence b
+};
+
+__device__ __forceinline__ int keys_of(const PagedParams& p, int b) { return min(max(p.len[b], 0), p.N); }
+
+__device__ __forceinline__ int64_t total_tiles(const PagedParams& p, int tk, int lane) {
+    int64_t sum = 0;
+    for (int b = lane; b < p.B; b += 32) sum += (keys_of(p, b) + tk - 1) / tk;
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(kFull, sum, w);
+    return sum * p.Hkv;
+}
+
+// where tile x (< total) of the list lies; called by whole warps
+__device__ __forceinline__ void locate(const PagedParams& p, int tk, int64_t x, int lane, Share& s) {
+    s.b = -1;
+    int64_t base = 0;  // tiles (of one head) before this round of 32 sequences
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        const int n = b < p.B ? keys_of(p, b) : 0;
+        const int nt = (n + tk - 1) / tk;
+        int64_t end = nt;
+#pragma unroll
+        for (int w = 1; w < 32; w <<= 1) {
+            const int64_t y = __shfl_up_sync(kFull, end, w);
+            if (lane >= w) end += y;
+        }
+        const int64_t first = (base + end - nt) * p.Hkv;
+        const unsigned hit = __ballot_sync(kFull, nt > 0 && x >= first && x < (base + end) * p.Hkv);
+        if (hit) {
+            const int at = __ffs(hit) - 1;
+            const int64_t f = __shfl_sync(kFull, first, at);
+            s.b = b0 + at;
+            s.n = __shfl_sync(kFull, n, at);
+            s.nt = __shfl_sync(kFull, nt, at);
+            s.h = (int)((x - f) / s.nt);
+            s.t = (int)((x - f) % s.nt);
+            s.unit0 = f + (int64_t)s.h * s.nt;
+            return;
+        }
+        base += __shfl_sync(kFull, end, 31);
+    }
+}
+
+// first sequence from b on that has keys (B: none)
+__device__ __forceinline__ int next_seq(const PagedParams& p, int b, int& n) {
+    while (b < p.B && (n = keys_of(p, b)) == 0) ++b;
+    return b;
+}
+
+// share c of `shares` (at most the number of tiles, so that none is empty)
+__device__ __forceinline__ int64_t share_begin(int64_t total, int64_t c, int64_t shares) { return total * c / shares; }
+
+template <class Tile>
+struct Smem {
+    static constexpr int kSlotFloats = Tile::G * (Tile::D + 2);
+    // merge slots: one a warp where they fit beside the ring twice an SM, else warps take turns
+    static constexpr int kRoom = 115712 - kWarps * kStages * kStageBytes - kWarps * (Tile::kScratchFloats + 1) * 4 - 256;
+    static constexpr int kSlots = 4 * kSlotFloats * 4 <= kRoom ? 4 : 2 * kSlotFloats * 4 <= kRoom ? 2 : 1;
+    alignas(128) uint8_t ring[kWarps][kStages][kStageBytes];
+    float slot[kSlots][kSlotFloats];
+    float scratch[kWarps][Tile::kScratchFloats + 1];
+    unsigned mask[kWarps][kStages];
+};
+
+template <class Tile>
+__global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
+    const typename Tile::T* __restrict__ q, const typename Tile::T* __restrict__ k_new,
+    const typename Tile::T* __restrict__ v_new, typename Tile::T* __restrict__ K, typename Tile::T* __restrict__ V,
+    typename Tile::T* __restrict__ out, float* __restrict__ lse, float* __restrict__ part, PagedParams p) {
+    using T = typename Tile::T;
+    constexpr int D = Tile::D, G = Tile::G, KT = Tile::KT, TK = kWarps * KT;
+    constexpr int CPR = Tile::RowBytes / 16, RPI = 32 / CPR;  // chunks a row, rows a warp copies at once
+    extern __shared__ __align__(128) uint8_t raw[];
+    Smem<Tile>& sm = *reinterpret_cast<Smem<Tile>*>(raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int grid = gridDim.x, cta = blockIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+
+    // empty sequences: nothing to attend to
+    for (int b = cta; b < p.B; b += grid)
+        if (keys_of(p, b) == 0) {
+            for (int i = tid; i < p.Hq * D; i += kWarps * 32) out[(size_t)b * p.Hq * D + i] = (T)0.f;
+            if (lse)
+                for (int i = tid; i < p.Hq; i += kWarps * 32) lse[(size_t)b * p.Hq + i] = -INFINITY;
+        }
+    const int64_t total = total_tiles(p, TK, lane);
+    const int64_t shares = min((int64_t)grid, total);
+    if (cta >= shares) return;
+    const int64_t x0 = share_begin(total, cta, shares), x1 = share_begin(total, cta + 1, shares);
+    Share at;
+    locate(p, TK, x0, lane, at);
+    if (at.b < 0) return;
+
+    // ---- the loading side: its own place in the list, kStages - 1 tiles ahead
+    int lb = at.b, lh = at.h, lt = at.t, ln = at.n, lnt = at.nt;
+    int64_t left = x1 - x0;  // tiles not yet issued
+    int page = -1;           // of this lane's row of the next tile (lanes < KT)
+    auto fetch = [&]() {
+        const int pos = lt * TK + warp * KT + lane;
+        page = left > 0 && lane < KT && pos < ln ? __ldg(p.table + (size_t)lb * p.W + pos / p.S) : -1;
+    };
+    auto issue = [&](int stage) {
+        if (left > 0) {
+            const int pos = lt * TK + warp * KT + lane;
+            const bool live = lane < KT && pos < ln && page >= 0 && page < p.P;
+            const int row = live ? (page * p.Hkv + lh) * p.S + pos % p.S : -1;  // of the pool (< 2^31)
+            const unsigned mask = __ballot_sync(kFull, live);
+            if (lane == 0) sm.mask[warp][stage] = mask;
+            const uint32_t kbuf = tc::smem_u32(sm.ring[warp][stage]), vbuf = kbuf + kStageBytes / 2;
+            const int c = lane % CPR;
+            const bool fresh = k_new != nullptr && (ln - 1) / TK == lt && ((ln - 1) % TK) / KT == warp;
+#pragma unroll
+            for (int i = 0; i < KT / RPI; ++i) {
+                const int r = i * RPI + lane / CPR;
+                const int src = __shfl_sync(kFull, row, r);
+                const size_t e = (size_t)max(src, 0) * D + c * (16 / sizeof(T));
+                const T *ks = K + e, *vs = V + e;
+                if (fresh && lt * TK + warp * KT + r == ln - 1) {  // the token in hand: from its rows, and into its page
+                    const size_t u = ((size_t)lb * p.Hkv + lh) * D + c * (16 / sizeof(T));
+                    ks = k_new + u;
+                    vs = v_new + u;
+                    if (src >= 0) {
+                        *reinterpret_cast<uint4*>(K + e) = __ldg(reinterpret_cast<const uint4*>(ks));
+                        *reinterpret_cast<uint4*>(V + e) = __ldg(reinterpret_cast<const uint4*>(vs));
+                    }
+                }
+                cp_async16_if(kbuf + ring_off<Tile::RowBytes>(r, c), ks, src >= 0);
+                cp_async16_if(vbuf + ring_off<Tile::RowBytes>(r, c), vs, src >= 0);
+            }
+            --left;
+            if (++lt == lnt) {
+                lt = 0;
+                if (++lh == p.Hkv) {
+                    lh = 0;
+                    lb = next_seq(p, lb + 1, ln);
+                    if (lb == p.B) left = 0;
+                    lnt = (ln + TK - 1) / TK;
+                }
+            }
+            fetch();
+        }
+        tc::cp_async_commit();
+    };
+    fetch();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+    // ---- the computing side
+    Tile tile;
+    tile.reset();
+    int b = at.b, h = at.h, t = at.t, n = at.n, nt = at.nt, t_first = at.t;
+    tile.load_q(q + ((size_t)b * p.Hq + (size_t)h * G) * D, p.qscale, lane);
+    int stage = 0, fill = kStages - 1;
+    for (int64_t x = x0; x < x1; ++x) {
+        tc::cp_async_wait_group<kStages - 2>();
+        __syncwarp();
+        const unsigned mask = sm.mask[warp][stage];
+        const uint32_t kbuf = tc::smem_u32(sm.ring[warp][stage]);
+        tile.step(kbuf, kbuf + kStageBytes / 2, mask, p.qscale, lane, sm.scratch[warp]);
+        __syncwarp();
+        issue(fill);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        fill = fill + 1 == kStages ? 0 : fill + 1;
+        ++t;
+        if (t < nt && x + 1 < x1) continue;
+        // the unit, or this CTA's part of it, is through: merge the warps
+        const bool whole = t_first == 0 && t == nt;
+        constexpr int NS = Smem<Tile>::kSlots;
+#pragma unroll
+        for (int r = 0; r < kWarps / NS; ++r) {
+            if (warp / NS == r) tile.put(sm.slot[warp % NS], r > 0, lane);
+            __syncthreads();
+        }
+        const size_t unit = (size_t)b * p.Hq + (size_t)h * G;
+        for (int i = tid; i < G * D / 4; i += kWarps * 32) {
+            const int hh = i / (D / 4), e = (i % (D / 4)) * 4;
+            float ms[NS], M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < NS; ++w) {
+                ms[w] = sm.slot[w][G * D + hh];
+                M = fmaxf(M, ms[w]);
+            }
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < NS; ++w) {
+                const float a = ms[w] == -INFINITY ? 0.f : exp2f(ms[w] - M);
+                const float* x4 = &sm.slot[w][hh * D + e];
+                sum += a * sm.slot[w][G * D + G + hh];
+                acc.x += a * x4[0];
+                acc.y += a * x4[1];
+                acc.z += a * x4[2];
+                acc.w += a * x4[3];
+            }
+            if (whole) {
+                const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;  // no key counted: 0
+                const float r[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+                store_vec<T, 4>(out + (unit + hh) * D + e, r);
+                if (lse && e == 0) lse[unit + hh] = (M + log2f(sum)) * kLn2;
+            } else {
+                // slot 0: a part that begins inside its unit; 1: one that ends inside it
+                const size_t at_part = ((size_t)cta * 2 + (t_first == 0 ? 1 : 0)) * G + hh;
+                *reinterpret_cast<float4*>(part + at_part * D + e) = acc;
+                if (e == 0) {
+                    float* ml = part + (size_t)grid * 2 * G * D + at_part * 2;
+                    ml[0] = M;
+                    ml[1] = sum;
+                }
+            }
+        }
+        __syncthreads();
+        if (x + 1 >= x1) break;
+        tile.reset();
+        t = t_first = 0;
+        if (++h == p.Hkv) {
+            h = 0;
+            b = next_seq(p, b + 1, n);
+            if (b == p.B) break;
+            nt = (n + TK - 1) / TK;
+        }
+        tile.load_q(q + ((size_t)b * p.Hq + (size_t)h * G) * D, p.qscale, lane);
+    }
+    tc::cp_async_wait_all();
+}
+
+// Joins the parts of the units that more than one CTA had a share of. CTA
+// (c, head): if share c begins inside a unit whose beginning lies in share
+// c - 1, the unit's parts are slot 1 of c - 1 and slot 0 of c, c + 1, ...
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(128) paged_join_kernel(T* __restrict__ out, float* __restrict__ lse,
+                                                         const float* __restrict__ part, int tk, PagedParams p) {
+    __shared__ float s_m[4], s_l[4];
+    __shared__ float4 s_o[4][D / 4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t grid = gridDim.x, c = blockIdx.x;
+    const int hh = blockIdx.y;
+    if (c == 0) return;
+    const int64_t total = total_tiles(p, tk, lane);
+    const int64_t shares = min(grid, total);
+    if (c >= shares) return;
+    Share at;
+    locate(p, tk, share_begin(total, c, shares), lane, at);
+    if (at.b < 0 || at.t == 0 || share_begin(total, c - 1, shares) > at.unit0) return;
+    const int64_t end = at.unit0 + at.nt;
+    // c - 1 and c, then every share that begins before the unit's end: the last such
+    // share is the one that holds tile end - 1
+    const int parts = (int)((end * shares - 1) / total - (c - 1)) + 1;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const float* ml = part + (size_t)grid * 2 * G * D;
+    auto row = [&](int i) { return ((size_t)(c - 1 + i) * 2 + (i == 0 ? 1 : 0)) * G + hh; };
+    float M = -INFINITY;
+    for (int i = tid; i < parts; i += 128) M = fmaxf(M, ml[row(i) * 2]);
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, w));
+    if (lane == 0) s_m[warp] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int i = warp; i < parts; i += 4) {  // a fixed order: the result does not depend on timing
+        const size_t r = row(i);
+        const float m = ml[r * 2], a = m == -INFINITY ? 0.f : exp2f(m - M);
+        sum += a * ml[r * 2 + 1];
+        if (lane < D / 4) {
+            const float4 v = *reinterpret_cast<const float4*>(part + r * D + lane * 4);
+            acc.x += a * v.x;
+            acc.y += a * v.y;
+            acc.z += a * v.z;
+            acc.w += a * v.w;
+        }
+    }
+    if (lane < D / 4) s_o[warp][lane] = acc;
+    if (lane == 0) s_l[warp] = sum;
+    __syncthreads();
+    if (tid < D / 4) {
+        sum = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+        const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+        const float4 a = s_o[0][tid], b = s_o[1][tid], cc = s_o[2][tid], d = s_o[3][tid];
+        const float r[4] = {((a.x + b.x) + (cc.x + d.x)) * inv, ((a.y + b.y) + (cc.y + d.y)) * inv,
+                            ((a.z + b.z) + (cc.z + d.z)) * inv, ((a.w + b.w) + (cc.w + d.w)) * inv};
+        const size_t u = (size_t)at.b * p.Hq + (size_t)at.h * G + hh;
+        store_vec<T, 4>(out + u * D + tid * 4, r);
+        if (lse && tid == 0) lse[u] = (M + log2f(sum)) * kLn2;
+    }
+}
+
+template <class Tile>
+cudaError_t launch_tile(const void* q, const void* k_new, const void* v_new, void* K, void* V, void* o, float* lse,
+                        float* part, const PagedParams& p, int sms, cudaStream_t st) {
+    using T = typename Tile::T;
+    constexpr int TK = kWarps * Tile::KT;
+    auto kern = paged_attn_kernel<Tile>;
+    const int smem = (int)sizeof(Smem<Tile>);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t per_unit = ((int64_t)p.N + TK - 1) / TK, most = (int64_t)p.B * p.Hkv * per_unit;
+    int64_t grid = 2 * (int64_t)sms;  // two CTAs an SM, all resident at once
+    if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
+    if (grid > most) grid = most;
+    kern<<<(unsigned)grid, kWarps * 32, smem, st>>>((const T*)q, (const T*)k_new, (const T*)v_new, (T*)K, (T*)V, (T*)o,
+                                                    lse, part, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || per_unit == 1 || grid == 1) return e;  // no unit can be cut
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, Tile::G);
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;  // the join's launch and its look at the lengths overlap the kernel above
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<T, Tile::D, Tile::G>, (T*)o, lse, (const float*)part, TK, p);
+}
+
+template <int D, int G>
+cudaError_t launch_dtype(int dtype, const void* q, const void* k_new, const void* v_new, void* K, void* V, void* o,
+                         float* lse, float* part, const PagedParams& p, int sms, cudaStream_t st) {
+    if (dtype == 1) return launch_tile<MmaTile<D, G>>(q, k_new, v_new, K, V, o, lse, part, p, sms, st);
+    return launch_tile<FmaTile<D, G>>(q, k_new, v_new, K, V, o, lse, part, p, sms, st);
+}
+
+template <int D>
+cudaError_t launch_group(int dtype, const void* q, const void* k_new, const void* v_new, void* K, void* V, void* o,
+                         float* lse, float* part, const PagedParams& p, int sms, cudaStream_t st) {
+    switch (p.Hq / p.Hkv) {
+        case 1: return launch_dtype<D, 1>(dtype, q, k_new, v_new, K, V, o, lse, part, p, sms, st);
+        case 2: return launch_dtype<D, 2>(dtype, q, k_new, v_new, K, V, o, lse, part, p, sms, st);
+        case 4: return launch_dtype<D, 4>(dtype, q, k_new, v_new, K, V, o, lse, part, p, sms, st);
+        case 8: return launch_dtype<D, 8>(dtype, q, k_new, v_new, K, V, o, lse, part, p, sms, st);
+        case 16: return launch_dtype<D, 16>(dtype, q, k_new, v_new, K, V, o, lse, part, p, sms, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attn(int dtype, int d, const void* q, const void* k_new, const void* v_new, void* K, void* V,
+                              void* o, float* lse, void* ws, const PagedParams& p, int sms, cudaStream_t st) {
+    float* part = (float*)ws;
+    if (d == 128) return launch_group<128>(dtype, q, k_new, v_new, K, V, o, lse, part, p, sms, st);
+    if (d == 64) return launch_group<64>(dtype, q, k_new, v_new, K, V, o, lse, part, p, sms, st);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace pisa

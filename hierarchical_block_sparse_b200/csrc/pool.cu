@@ -17,7 +17,9 @@ __device__ __forceinline__ int64_t keys_of(const PoolParams& p, int64_t b) {
     return n < 0 ? 0 : (n > p.k_rows ? p.k_rows : n);
 }
 
-template <typename T, int D>
+// PAGED: K is a pool [P, Hkv, S, D] whose pages hold whole leaves, so a leaf's rows
+// are one run of memory; a leaf without a page counts as zeros.
+template <typename T, int D, bool PAGED>
 __global__ void __launch_bounds__(256) pool_leaves_kernel(const T* __restrict__ K, float* __restrict__ pyr,
                                                           PoolParams p) {
     constexpr int E = Ld16<T>::E;   // elements per 16-byte load
@@ -30,7 +32,7 @@ __global__ void __launch_bounds__(256) pool_leaves_kernel(const T* __restrict__ 
     const int64_t bh = blockIdx.y;
     const int64_t len = keys_of(p, bh / p.Hkv);
     const int C = p.C;
-    const T* Kh = K + bh * p.k_rows * D;
+    const T* Kh = PAGED ? K : K + bh * p.k_rows * D;
     float* P = pyr + bh * p.geom.rows * D;
     const int64_t leaf0 = (int64_t)blockIdx.x * LPC;
     const int64_t live_leaves = (len + C - 1) / C;
@@ -44,6 +46,11 @@ __global__ void __launch_bounds__(256) pool_leaves_kernel(const T* __restrict__ 
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
         int64_t r = lo + rsub;
+        if constexpr (PAGED) {
+            const int tok = (int)lo, page = __ldg(p.table + bh / p.Hkv * p.W + tok / p.S);
+            if ((unsigned)page >= (unsigned)p.P) r = hi;
+            Kh = K + (((int64_t)page * p.Hkv + bh % p.Hkv) * p.S + tok % p.S - lo) * D;  // row r is token r of the leaf
+        }
         for (; r + 3 * RPW < hi; r += 4 * RPW) {
             float x0[E], x1[E], x2[E], x3[E];
             Ld16<T>::run(Kh + r * D + col, x0);
@@ -120,7 +127,10 @@ template <typename T, int D>
 static cudaError_t launch_pool_t(const void* K, float* pyr, const PoolParams& p, cudaStream_t st) {
     const int64_t M1 = p.geom.M[1];
     dim3 grid((unsigned)((M1 + kLeavesPerCta - 1) / kLeavesPerCta), (unsigned)(p.B * p.Hkv));
-    pool_leaves_kernel<T, D><<<grid, 256, 0, st>>>((const T*)K, pyr, p);
+    if (p.table)
+        pool_leaves_kernel<T, D, true><<<grid, 256, 0, st>>>((const T*)K, pyr, p);
+    else
+        pool_leaves_kernel<T, D, false><<<grid, 256, 0, st>>>((const T*)K, pyr, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int first = 2 + 4;  // log2(kLeavesPerCta) = 4 levels above the leaves done in-CTA

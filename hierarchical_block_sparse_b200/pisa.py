@@ -34,6 +34,10 @@ class PisaCfg(ctypes.Structure):
                 ("B", "Hq", "Hkv", "N", "d", "C", "K", "g", "causal", "forced_mask", "dtype", "score_variant")]
 
 
+class PisaPages(ctypes.Structure):
+    _fields_ = [("S", ctypes.c_int32), ("P", ctypes.c_int32)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -60,6 +64,8 @@ def load(path: str | None = None):
         lib = ctypes.CDLL(p)
         P = ctypes.c_void_p
         cfgp = ctypes.POINTER(PisaCfg)
+        pgp = ctypes.POINTER(PisaPages)
+        I64 = ctypes.c_int64
         sig = {
             "pisa_num_levels": (ctypes.c_int, [cfgp]),
             "pisa_level_nodes": (ctypes.c_int64, [cfgp, ctypes.c_int]),
@@ -95,6 +101,18 @@ def load(path: str | None = None):
                                                                    ctypes.POINTER(ctypes.c_void_p), ctypes.c_int, P]),
             "pisa_decode": (ctypes.c_int, [cfgp, P, P, P, P, P, P, P, P]),
             "pisa_decode_step": (ctypes.c_int, [cfgp, P, P, P, P, P, P, P, P, P, P]),
+            "pisa_pages_state_words": (I64, [pgp]),
+            "pisa_pages_init": (ctypes.c_int, [cfgp, pgp, P, P, P, P]),
+            "pisa_pages_reserve": (ctypes.c_int, [cfgp, pgp, P, P, P, P, P, P, I64, P]),
+            "pisa_pages_fork": (ctypes.c_int, [cfgp, pgp, P, P, P, P, P, P, P]),
+            "pisa_pages_free": (ctypes.c_int, [cfgp, pgp, P, ctypes.c_int, P, P, P, P]),
+            "pisa_pages_compact": (ctypes.c_int, [cfgp, pgp, P, P, P, I64, P]),
+            "pisa_pages_copy": (ctypes.c_int, [cfgp, pgp, P, I64, P, P, P]),
+            "pisa_paged_append": (ctypes.c_int, [cfgp, pgp, P, P, ctypes.c_int, P, P, P, P, P, P]),
+            "pisa_paged_workspace_bytes": (I64, [cfgp, pgp]),
+            "pisa_paged_attn": (ctypes.c_int, [cfgp, pgp, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]),
+            "pisa_paged_build_pyramid": (ctypes.c_int, [cfgp, pgp, P, P, P, P, P]),
+            "pisa_paged_decode_step": (ctypes.c_int, [cfgp, pgp, P, P, P, P, P, P, P, P, P, P, P]),
             "pisa_fma_probe": (ctypes.c_int, [P, ctypes.c_int, ctypes.c_int, ctypes.c_int, P]),
             "pisa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "pisa_version": (ctypes.c_char_p, []),
@@ -405,6 +423,228 @@ def pisa_decode_step(cfg, q_new, k_new, v_new, Kc, Vc, pyr, pos, idx, o):
     _check("pisa_decode_step", load().pisa_decode_step(ctypes.byref(cfg), _ptr(q_new), _ptr(k_new), _ptr(v_new),
                                                        _ptr(Kc), _ptr(Vc), _ptr(pyr), _ptr(pos), _ptr(idx), _ptr(o),
                                                        _stream()))
+
+
+# ---- paged decode cache ---------------------------------------------------------------
+
+def make_pages(S: int, P: int) -> PisaPages:
+    """S tokens per page, P pages in the pool."""
+    return PisaPages(int(S), int(P))
+
+
+def pages_width(cfg, pages) -> int:
+    """W: table entries per sequence."""
+    return -(-cfg.N // pages.S)
+
+
+def pisa_pages_state_words(pages) -> int:
+    r = int(load().pisa_pages_state_words(ctypes.byref(pages)))
+    if r < 0:
+        _check("pisa_pages_state_words", r)
+    return r
+
+
+def _elem(cfg):
+    return torch.bfloat16 if cfg.dtype == PISA_DTYPE_BF16 else torch.float32
+
+
+def _pool(cfg, pages):
+    return pages.P * cfg.Hkv * pages.S * cfg.d
+
+
+def _paged(name: str, cfg, pages, *args) -> None:
+    """Call `name` with tensors given as (tensor, dtype, least number of elements) and
+    plain numbers as they are, on the tensors' device and its current stream."""
+    dev, out = None, []
+    for a in args:
+        if type(a) is not tuple:
+            out.append(a)
+            continue
+        t, dtype, n = a
+        if t is None:
+            out.append(None)
+            continue
+        if dev is None:
+            dev = t.device
+            if dev.type != "cuda":
+                raise ValueError("tensors must live on a CUDA device")
+        elif t.device != dev:
+            raise ValueError(f"{name}: tensors on different devices ({dev}, {t.device})")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        if t.dtype is not dtype or t.numel() < n:
+            raise ValueError(f"{name}: expected at least {n} elements of {dtype}, got {t.numel()} of {t.dtype}")
+        out.append(t.data_ptr())
+    fn = getattr(load(), name)
+    if dev.index == torch.cuda.current_device():
+        status = fn(cfg, pages, *out, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(cfg, pages, *out, torch.cuda.current_stream().cuda_stream)
+    if status != 0:
+        _check(name, status)
+
+
+def pisa_pages_init(cfg, pages, state, table, lens):
+    """An empty cache: every page free, table -1, lengths 0."""
+    i32 = torch.int32
+    _paged("pisa_pages_init", cfg, pages, (state, i32, pisa_pages_state_words(pages)),
+           (table, i32, cfg.B * pages_width(cfg, pages)), (lens, i32, cfg.B))
+
+
+def pisa_pages_reserve(cfg, pages, add, state, table, lens, grant, moves):
+    """Room for add[b] more tokens of each sequence; lens grows by grant[b]."""
+    i32, B = torch.int32, cfg.B
+    _paged("pisa_pages_reserve", cfg, pages, (add, i32, B), (state, i32, pisa_pages_state_words(pages)),
+           (table, i32, B * pages_width(cfg, pages)), (lens, i32, B), (grant, i32, B), (moves, i32, 4), moves.numel())
+
+
+def pisa_pages_fork(cfg, pages, parent, state, table, lens, table_out, lens_out):
+    """Sequence b becomes a copy of sequence parent[b] (outside [0, B): it ends), sharing its pages."""
+    i32, B = torch.int32, cfg.B
+    n = B * pages_width(cfg, pages)
+    _paged("pisa_pages_fork", cfg, pages, (parent, i32, B), (state, i32, pisa_pages_state_words(pages)), (table, i32, n),
+           (lens, i32, B), (table_out, i32, n), (lens_out, i32, B))
+
+
+def pisa_pages_free(cfg, pages, seqs, state, table, lens):
+    """Ends the listed sequences."""
+    i32, B = torch.int32, cfg.B
+    _paged("pisa_pages_free", cfg, pages, (seqs, i32, 0), seqs.numel(), (state, i32, pisa_pages_state_words(pages)),
+           (table, i32, B * pages_width(cfg, pages)), (lens, i32, B))
+
+
+def pisa_pages_compact(cfg, pages, state, table, moves):
+    """Moves the live pages to the low end of the pool; `moves` lists the copies to make."""
+    i32 = torch.int32
+    _paged("pisa_pages_compact", cfg, pages, (state, i32, pisa_pages_state_words(pages)),
+           (table, i32, cfg.B * pages_width(cfg, pages)), (moves, i32, 4), moves.numel())
+
+
+def pisa_pages_copy(cfg, pages, moves, K, V):
+    """Copies the pages of one layer as `moves` lists them."""
+    dt, n = _elem(cfg), _pool(cfg, pages)
+    _paged("pisa_pages_copy", cfg, pages, (moves, torch.int32, 4), moves.numel(), (K, dt, n), (V, dt, n))
+
+
+def pisa_paged_append(cfg, pages, k_new, v_new, lens, count, table, K, V):
+    """Writes rows k_new[b, :, i], v_new[b, :, i] ([B, Hkv, T, d], or [B, Hkv, d]), i < count[b], as the
+    last count[b] of the sequence's lens[b] tokens."""
+    i32, dt, B, n = torch.int32, _elem(cfg), cfg.B, _pool(cfg, pages)
+    T = k_new.shape[2] if k_new.dim() == 4 else 1
+    rows = B * cfg.Hkv * T * cfg.d
+    _paged("pisa_paged_append", cfg, pages, (k_new, dt, rows), (v_new, dt, rows), T, (lens, i32, B), (count, i32, B),
+           (table, i32, B * pages_width(cfg, pages)), (K, dt, n), (V, dt, n))
+
+
+def pisa_paged_workspace_bytes(cfg, pages) -> int:
+    r = int(load().pisa_paged_workspace_bytes(ctypes.byref(cfg), ctypes.byref(pages)))
+    if r < 0:
+        _check("pisa_paged_workspace_bytes", r)
+    return r
+
+
+def alloc_paged_workspace(cfg, pages, device="cuda") -> torch.Tensor:
+    """Caller-owned workspace for pisa_paged_attn."""
+    return torch.empty(pisa_paged_workspace_bytes(cfg, pages), dtype=torch.uint8, device=device)
+
+
+def pisa_paged_attn(cfg, pages, q, k_new, v_new, K, V, table, lens, o, lse, ws):
+    """Dense attention of one token a sequence over its paged cache (k_new, v_new given: appended on the way)."""
+    i32, dt, B, n, d = torch.int32, _elem(cfg), cfg.B, _pool(cfg, pages), cfg.d
+    _paged("pisa_paged_attn", cfg, pages, (q, dt, B * cfg.Hq * d), (k_new, dt, B * cfg.Hkv * d),
+           (v_new, dt, B * cfg.Hkv * d), (K, dt, n), (V, dt, n), (table, i32, B * pages_width(cfg, pages)),
+           (lens, i32, B), (o, dt, B * cfg.Hq * d), (lse, torch.float32, B * cfg.Hq), (ws, torch.uint8, 0), ws.numel())
+
+
+def pisa_paged_build_pyramid(cfg, pages, K, table, lens, pyr):
+    """pisa_build_pyramid_prefix from a paged cache; sequences with lens[b] <= 0 are left untouched."""
+    i32, B = torch.int32, cfg.B
+    _paged("pisa_paged_build_pyramid", cfg, pages, (K, _elem(cfg), _pool(cfg, pages)),
+           (table, i32, B * pages_width(cfg, pages)), (lens, i32, B),
+           (pyr, torch.float32, B * cfg.Hkv * pisa_pyramid_rows(cfg) * cfg.d))
+
+
+def pisa_paged_decode_step(cfg, pages, q_new, k_new, v_new, K, V, table, lens, pyr, idx, o):
+    """pisa_decode_step over a paged cache; the token in hand is token lens[b] - 1."""
+    i32, dt, B, n, d = torch.int32, _elem(cfg), cfg.B, _pool(cfg, pages), cfg.d
+    _paged("pisa_paged_decode_step", cfg, pages, (q_new, dt, B * cfg.Hq * d), (k_new, dt, B * cfg.Hkv * d),
+           (v_new, dt, B * cfg.Hkv * d), (K, dt, n), (V, dt, n), (table, i32, B * pages_width(cfg, pages)),
+           (lens, i32, B), (pyr, torch.float32, B * cfg.Hkv * pisa_pyramid_rows(cfg) * d), (idx, i32, B * cfg.Hkv * cfg.K),
+           (o, dt, B * cfg.Hq * d))
+
+
+class PagedCache:
+    """A decode cache in pages: pools K, V [P, Hkv, S, d] and, for the sparse step, a
+    pyramid, for each layer; one table, lengths and page state for all of them.
+    cfg.N is the most tokens a sequence may hold. No call reads device memory on
+    the host; `moves[1]` (pages missing at the last reserve) is for the caller to read."""
+
+    def __init__(self, cfg, pages, layers: int = 1, sparse: bool = True, device="cuda"):
+        self.cfg, self.pages = cfg, pages
+        dt, W = _elem(cfg), pages_width(cfg, pages)
+        shape = (pages.P, cfg.Hkv, pages.S, cfg.d)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.K = [torch.empty(shape, dtype=dt, device=device) for _ in range(layers)]
+        self.V = [torch.empty(shape, dtype=dt, device=device) for _ in range(layers)]
+        self.pyr = [torch.empty((cfg.B, cfg.Hkv, pisa_pyramid_rows(cfg), cfg.d), dtype=torch.float32, device=device)
+                    for _ in range(layers if sparse else 0)]
+        self.state = torch.empty(pisa_pages_state_words(pages), **i32)
+        self.table, self.lens = torch.empty((cfg.B, W), **i32), torch.empty(cfg.B, **i32)
+        self._table, self._lens = torch.empty_like(self.table), torch.empty_like(self.lens)  # fork's other buffers
+        self.grant = torch.zeros(cfg.B, **i32)
+        self.moves = torch.zeros(4 + 2 * max(cfg.B, pages.P // 2), **i32)
+        self.ws = alloc_paged_workspace(cfg, pages, device)
+        pisa_pages_init(cfg, pages, self.state, self.table, self.lens)
+
+    def _copy(self) -> None:
+        for K, V in zip(self.K, self.V):
+            pisa_pages_copy(self.cfg, self.pages, self.moves, K, V)
+
+    def reserve(self, add: torch.Tensor) -> torch.Tensor:
+        """Room for add[b] more tokens; returns grant (the tokens each sequence got)."""
+        pisa_pages_reserve(self.cfg, self.pages, add, self.state, self.table, self.lens, self.grant, self.moves)
+        self._copy()
+        return self.grant
+
+    def append(self, k_new, v_new, layer: int = 0, count: torch.Tensor | None = None) -> None:
+        """Rows of the tokens granted last (or of `count`) into the pages."""
+        pisa_paged_append(self.cfg, self.pages, k_new, v_new, self.lens, self.grant if count is None else count,
+                          self.table, self.K[layer], self.V[layer])
+
+    def build_pyramid(self, layer: int = 0, lens: torch.Tensor | None = None) -> None:
+        """Summaries of what is cached (or of lens[b] tokens; <= 0: left as they are)."""
+        pisa_paged_build_pyramid(self.cfg, self.pages, self.K[layer], self.table, self.lens if lens is None else lens,
+                                 self.pyr[layer])
+
+    def attend(self, q, o, lse=None, k_new=None, v_new=None, layer: int = 0) -> None:
+        """Dense attention of one token a sequence (its rows appended on the way when given)."""
+        pisa_paged_attn(self.cfg, self.pages, q, k_new, v_new, self.K[layer], self.V[layer], self.table, self.lens, o, lse,
+                        self.ws)
+
+    def step(self, q_new, k_new, v_new, idx, o, layer: int = 0) -> None:
+        """The sparse step (append, select, attend) for the token reserved last."""
+        pisa_paged_decode_step(self.cfg, self.pages, q_new, k_new, v_new, self.K[layer], self.V[layer], self.table,
+                               self.lens, self.pyr[layer], idx, o)
+
+    def fork(self, parent: torch.Tensor) -> None:
+        """Sequence b becomes a copy of sequence parent[b]; pyramids of the new ones are rebuilt."""
+        pisa_pages_fork(self.cfg, self.pages, parent, self.state, self.table, self.lens, self._table, self._lens)
+        self.table, self._table, self.lens, self._lens = self._table, self.table, self._lens, self.lens
+        if self.pyr:
+            same = parent == torch.arange(self.cfg.B, dtype=torch.int32, device=parent.device)
+            lens = self.lens.masked_fill(same, 0)
+            for layer in range(len(self.pyr)):
+                self.build_pyramid(layer, lens)
+
+    def free(self, seqs: torch.Tensor) -> None:
+        """Ends the listed sequences."""
+        pisa_pages_free(self.cfg, self.pages, seqs, self.state, self.table, self.lens)
+
+    def compact(self) -> None:
+        """Moves the live pages of every layer to the low end of the pools."""
+        pisa_pages_compact(self.cfg, self.pages, self.state, self.table, self.moves)
+        self._copy()
 
 
 def pisa_status_string(status: int) -> str:

@@ -375,6 +375,124 @@ int pisa_decode_step(const pisa_cfg *cfg, const void *q_new, const void *k_new, 
                      void *Kc, void *Vc, float *pyr, const int32_t *pos, int32_t *idx, void *o,
                      void *stream);
 
+/* ---- paged decode cache ----------------------------------------------------------
+ * The decode cache in pages, for serving: sequences grow without copies, share
+ * the pages of a common prefix, and give them back when they end. (The pages
+ * describe one contiguous cache, close reading §5.3; the paging itself has no
+ * counterpart there.) In these calls cfg->N is the most tokens a sequence may
+ * hold, and
+ *   K, V:  pools [P, Hkv, S, d] of cfg->dtype: P pages of S tokens;
+ *   table: int32 [B, W], W = ceil(N / S): page of tokens [w*S, (w+1)*S) of
+ *          sequence b, -1 where it has none;
+ *   len:   int32 [B], tokens of each sequence, those being added included;
+ *   state: int32 [pisa_pages_state_words(pages)], 16-byte aligned: the number of
+ *          table entries that name each page [P], then, from word 4*ceil(P/4) on,
+ *          the bitmap of free pages (bit j of word i: page 32 i + j), then room
+ *          for the calls themselves;
+ *   moves: int32 list of page copies: words 0..3 hold their number, the pages
+ *          missing, the live and the free pages; then (source, destination) pairs.
+ * Table, lengths and state serve all layers of a model; K and V are one layer's.
+ * All of them are device memory. The calls that read them check what they read: a
+ * token whose table entry is outside [0, P) counts as absent, is not read and
+ * is not written; lengths are clamped to [0, N]. A pool row past a sequence's
+ * length is never used, whatever it holds (NaN included).
+ * Limits: those of the decode calls, 1 <= S <= 1024, P*Hkv*S < 2^31, B*W < 2^31.
+ * The pyramid calls need S to be a multiple of C. */
+typedef struct pisa_pages {
+    int32_t S;  /* tokens per page */
+    int32_t P;  /* pages in the pool */
+} pisa_pages;
+
+/* Words of `state` (negative status on error). */
+int64_t pisa_pages_state_words(const pisa_pages *pages);
+
+/* An empty cache: every page free, table -1, lengths 0. */
+int pisa_pages_init(const pisa_cfg *cfg, const pisa_pages *pages, int32_t *state, int32_t *table, int32_t *len,
+                    void *stream);
+
+/* Room for add[b] more tokens of each sequence (int32 [B]; <= 0: none), as if
+ * done one sequence after another: the pages that len[b] + add[b] tokens need
+ * beyond those it has, lowest free page first, and, in place of a partially
+ * filled last page that other sequences hold too, a page of its own, listed in
+ * `moves` for pisa_pages_copy (which has to run, for every layer, before the
+ * tokens are written). grant[b] (int32 [B], written) is add[b], len[b] grows by it.
+ * A sequence that would pass N tokens, or whose last page is missing, gets grant
+ * 0 and is left as it is. When the free pages do not suffice no sequence gets
+ * any: all grants are 0, nothing changes, and moves[1] is the number of pages
+ * missing. The result does not depend on timing. moves_words >= 4 + 2*B;
+ * B <= 4096 (else PISA_E_UNSUPPORTED). */
+int pisa_pages_reserve(const pisa_cfg *cfg, const pisa_pages *pages, const int32_t *add, int32_t *state, int32_t *table,
+                       int32_t *len, int32_t *grant, int32_t *moves, int64_t moves_words, void *stream);
+
+/* Sequence b becomes a copy of sequence parent[b] (int32 [B]; b itself: it stays;
+ * outside [0, B): it ends), for all b at once, so parents may be repeated,
+ * swapped or chained. table_out [B, W] and len_out [B] are written; table and len
+ * are the old ones, to be given up. Pages are shared, not copied (see
+ * pisa_pages_reserve); pages that no sequence names any more become free.
+ * table_out == table or len_out == len gives PISA_E_INVALID. */
+int pisa_pages_fork(const pisa_cfg *cfg, const pisa_pages *pages, const int32_t *parent, int32_t *state,
+                    const int32_t *table, const int32_t *len, int32_t *table_out, int32_t *len_out, void *stream);
+
+/* Ends the n sequences seqs[] (int32, device): their entries become -1 and their
+ * lengths 0; pages that no sequence names any more become free. A sequence
+ * listed twice is freed once; one outside [0, B) is skipped. */
+int pisa_pages_free(const pisa_cfg *cfg, const pisa_pages *pages, const int32_t *seqs, int n, int32_t *state,
+                    int32_t *table, int32_t *len, void *stream);
+
+/* Moves the live pages to ids [0, L), L = live pages: the i-th live page at or
+ * past L goes to the i-th free one below it; table and state follow, and the
+ * moves are listed in ascending order for pisa_pages_copy. moves_words >=
+ * 4 + 2*(P / 2). */
+int pisa_pages_compact(const pisa_cfg *cfg, const pisa_pages *pages, int32_t *state, int32_t *table, int32_t *moves,
+                       int64_t moves_words, void *stream);
+
+/* Copies the K and V pages of one layer as `moves` lists them. No page may be
+ * both a source and a destination (the lists above never hold such). Pairs
+ * outside the pool are skipped; at most (moves_words - 4) / 2 pairs are read. */
+int pisa_pages_copy(const pisa_cfg *cfg, const pisa_pages *pages, const int32_t *moves, int64_t moves_words, void *K,
+                    void *V, void *stream);
+
+/* Writes the last count[b] (int32 [B]) of each sequence's len[b] tokens into its
+ * pages: rows k_new[b, :, i], v_new[b, :, i] ([B, Hkv, T, d], the layout of the
+ * prefill's K and V), i < count[b], are tokens len[b] - count[b] + i. A count
+ * outside [0, min(T, len[b])], or a length past N, leaves the sequence untouched. */
+int pisa_paged_append(const pisa_cfg *cfg, const pisa_pages *pages, const void *k_new, const void *v_new, int T,
+                      const int32_t *len, const int32_t *count, const int32_t *table, void *K, void *V, void *stream);
+
+/* Bytes of workspace pisa_paged_attn needs (negative status on error). */
+int64_t pisa_paged_workspace_bytes(const pisa_cfg *cfg, const pisa_pages *pages);
+
+/* Dense attention of one token a sequence over its whole paged cache (close
+ * reading §02: the softmax that Eq.(2) restricts): for query head h of sequence
+ * b, softmax(q . k_j / sqrt(d)) over j < len[b], applied to V. The dense
+ * counterpart of pisa_paged_decode_step, for dense layers, short sequences and
+ * comparisons. q: [B, Hq, d]; o: [B, Hq, d] (written, dtype); lse: fp32 [B, Hq]
+ * (written; may be NULL), the natural log of the sum of exponentials. A
+ * sequence without keys gives o = 0, lse = -inf. With k_new, v_new ([B, Hkv, d];
+ * both or neither) the token len[b] - 1 is written into its page on the way, as
+ * pisa_paged_append with T = 1 would. C, K, g, forced_mask and score_variant
+ * do not matter. Equal inputs give equal bits. workspace: 16-byte aligned,
+ * contents arbitrary, nothing is kept in it; calls that share one must not
+ * overlap on the GPU. */
+int pisa_paged_attn(const pisa_cfg *cfg, const pisa_pages *pages, const void *q, const void *k_new, const void *v_new,
+                    void *K, void *V, const int32_t *table, const int32_t *len, void *o, float *lse, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/* pisa_build_pyramid_prefix from a paged cache: summaries of the first len[b]
+ * tokens, laid out for N. Sequences with len[b] <= 0 are left untouched (so a
+ * forked sequence's pyramid can be built alone). S % C != 0 gives
+ * PISA_E_UNSUPPORTED. */
+int pisa_paged_build_pyramid(const pisa_cfg *cfg, const pisa_pages *pages, const void *K, const int32_t *table,
+                             const int32_t *len, float *pyr, void *stream);
+
+/* pisa_decode_step over a paged cache: the same kernel and results, the token
+ * being token len[b] - 1 (pos = len - 1). A sequence with len[b] outside [1, N], or
+ * without a page for the token, gets idx = -1 and o = 0 and is left untouched.
+ * S % C != 0 gives PISA_E_UNSUPPORTED. */
+int pisa_paged_decode_step(const pisa_cfg *cfg, const pisa_pages *pages, const void *q_new, const void *k_new,
+                           const void *v_new, void *K, void *V, const int32_t *table, const int32_t *len, float *pyr,
+                           int32_t *idx, void *o, void *stream);
+
 /* ---- misc --------------------------------------------------------------------- */
 
 /* Static English text for a status code (never NULL). */
