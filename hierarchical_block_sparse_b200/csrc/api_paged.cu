@@ -40,12 +40,6 @@ PagedParams params(const pisa_cfg* c, const pisa_pages* g, const int32_t* table,
 
 int elem_bytes(const pisa_cfg* c) { return c->dtype == PISA_DTYPE_BF16 ? 2 : 4; }
 
-int sm_count() {
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-}
-
 }  // namespace
 
 extern "C" {

@@ -6,7 +6,8 @@
 // units). The work is a list of tiles of TK keys, ordered by (sequence, KV
 // head, position); CTA c of `grid` takes the c-th equal share of that list,
 // whatever the lengths, so one long sequence and many short ones load the
-// GPU alike. A (sequence, KV head) unit that falls into one share is finished
+// GPU alike. Beginning and ending a (sequence, KV head) unit costs about as
+// much as a tile, which the list counts in front of the unit's own (kUnitCost). A (sequence, KV head) unit that falls into one share is finished
 // by its CTA; one that is cut leaves (max, sum, unnormalised o) of each part in
 // the workspace, which paged_join_kernel joins in share order (the result
 // depends on the lengths alone, not on timing).
@@ -25,6 +26,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kStages = 3;
 constexpr int kStageBytes = 8192;  // KT key rows, then KT value rows
+constexpr int kUnitCost = 1;  // 0: 104 us, 1: 77.6, 2: 78.9, 4: 83.1 for 64 sequences of 0..15 K tokens, 32 / 8 heads
 constexpr float kRescale = 8.f;    // see softmax below
 constexpr float kTiny = 1.17549435e-38f;  // smallest normal number
 
@@ -51,6 +53,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// an 8 x 8 matrix of 16-bit elements, two neighbours of a row a lane, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -65,15 +73,17 @@ __device__ __forceinline__ uint32_t ring_off(int r, int c) {
 
 // ---- one warp's tile, bf16: tensor cores -------------------------------------------
 //
-// S = Q K^T and O += P V as m16n8k16 products whose 16 rows are the group's
-// query heads. Decode needs 4 G products a key element pair against 4 bytes of
-// it, far below what even these instructions do per byte of HBM traffic, so the
-// shapes are chosen for short latency and few registers. P enters as bf16 high
-// and low parts (2^-16 relative): in one rounding its error would be as large as
-// the output's own. The high part is cut, not rounded, and the low part is kept
-// above zero, so that an infinite value times both stays that infinity. With
-// G <= 8 the low parts ride in the tile's unused rows 8..15 and cost nothing;
-// G = 16 takes a second product.
+// S^T = K Q^T and O^T += V^T P^T as m16n8k16 products: the keys (then the dims) are the
+// 16 rows and the group's heads the 8 columns, so a group of up to 8 heads takes half
+// of the products that heads as rows would (G <= 4: 16 instead of 32 a 16 keys). Decode
+// needs 4 G products a key element against 4 bytes of it, far below what even these
+// instructions do per byte of HBM traffic; what they cost is power, and the
+// kernel runs at the power limit.
+// P enters as bf16 high and low parts (2^-16 relative): in one rounding its error would
+// be as large as the output's own. The high part is cut, not rounded, and the low part
+// is kept above zero, so that an infinite value times both stays that infinity. With
+// G <= 4 the columns 4..7 repeat the heads 0..3 and carry the low parts, which then
+// cost nothing; larger groups take a second product.
 template <int D_, int G_>
 struct MmaTile {
     using T = __nv_bfloat16;
@@ -81,129 +91,144 @@ struct MmaTile {
     static constexpr int KT = kStageBytes / (2 * D * 2);  // 16 (d = 128) or 32 (d = 64) keys
     static constexpr int RowBytes = D * 2;
     static constexpr int kScratchFloats = 0;
-    static constexpr int RB = G > 8 ? 2 : 1;  // accumulator row blocks that hold heads
+    static constexpr int NT = G > 8 ? 2 : 1;    // column tiles
+    static constexpr bool kTwin = G <= 4;       // columns 4..7 repeat the heads for the low parts
 
-    uint32_t qa[D / 16][4];
-    float o[D / 8][4];
-    float m[RB], l[RB];
+    uint32_t qb[D / 16][NT][2];
+    float o[D / 16][NT][4];  // dims 16 j + g (+ 8), columns 2 c, 2 c + 1 (g = lane / 4, c = lane % 4)
+    float m[NT][2], l[NT][2];  // of this lane's columns; l is this lane's share
 
-    __device__ __forceinline__ void load_q(const T* q, float, int lane) {
+    static constexpr bool kAhead = NT == 1;  // registers for the next unit's queries
+    uint32_t qn[kAhead ? D / 16 : 1][NT][2];
+
+    static __device__ __forceinline__ void read_q(uint32_t (*to)[NT][2], const T* q, int lane) {
         const int g = lane >> 2, c = lane & 3;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int h = g + (i & 1) * 8, e = k * 16 + 2 * c + (i >> 1) * 8;
-                qa[k][i] = h < G ? __ldg(reinterpret_cast<const unsigned*>(q + (size_t)h * D + e)) : 0u;
-            }
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int h = kTwin ? g & 3 : 8 * t + g, e = k * 16 + 2 * c + 8 * i;
+                    to[k][t][i] = h < G ? __ldg(reinterpret_cast<const unsigned*>(q + (size_t)h * D + e)) : 0u;
+                }
+    }
+    __device__ __forceinline__ void load_q(const T* q, float, int lane) { read_q(qb, q, lane); }
+    // the next unit's queries: fetched early, taken when their unit begins
+    __device__ __forceinline__ void fetch_q(const T* q, int lane) {
+        if constexpr (kAhead) read_q(qn, q, lane);
+    }
+    __device__ __forceinline__ void take_q(const T* q, float, int lane) {
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) qb[k][0][i] = qn[k][0][i];
+        } else {
+            read_q(qb, q, lane);
+        }
     }
     __device__ __forceinline__ void reset() {
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)
+        for (int t = 0; t < NT; ++t) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+            for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-            m[i] = -INFINITY;
-            l[i] = 0.f;
+                for (int i = 0; i < 4; ++i) o[j][t][i] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[t][i] = -INFINITY;
+                l[t][i] = 0.f;
+            }
         }
     }
     // keys of this tile whose bit is set in `mask` count
     __device__ __forceinline__ void step(uint32_t kbuf, uint32_t vbuf, unsigned mask, float qscale, int lane, float*) {
-        const int c = lane & 3;
-        float s[KT / 8][4];
+        const int g = lane >> 2, c = lane & 3;
+        float s[KT / 16][NT][4];
 #pragma unroll
-        for (int j = 0; j < KT / 8; ++j) {
+        for (int r = 0; r < KT / 16; ++r) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[j][i] = 0.f;
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-                uint32_t b[4];
-                ldsm4(kbuf + ring_off<RowBytes>(8 * j + (lane & 7), 4 * k + (lane >> 3)), b);
-                mma16816(s[j], qa[2 * k], b[0], b[1]);
-                mma16816(s[j], qa[2 * k + 1], b[2], b[3]);
+                for (int i = 0; i < 4; ++i) s[r][t][i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t a[4];
+                ldsm4(kbuf + ring_off<RowBytes>(16 * r + (lane & 15), 2 * k + (lane >> 4)), a);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma16816(s[r][t], a, qb[k][t][0], qb[k][t][1]);
             }
         }
         // Running maximum: it is only moved when a logit passes it by more than
         // kRescale (the terms then stay below 2^8, far from overflow), so most tiles
-        // skip the rescaling of o.
-        float mx[RB];
+        // need neither the exchange between lanes nor the rescaling of o.
+        float mx[NT][2];
         bool move = false;
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-            mx[i] = -INFINITY;
+        for (int t = 0; t < NT; ++t) {
+            mx[t][0] = mx[t][1] = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < KT / 8; ++j)
+            for (int r = 0; r < KT / 16; ++r)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const bool live = (mask >> (8 * j + 2 * c + e)) & 1u;
-                    s[j][2 * i + e] = live ? s[j][2 * i + e] * qscale : -INFINITY;
-                    mx[i] = fmaxf(mx[i], s[j][2 * i + e]);
+                for (int i = 0; i < 4; ++i) {
+                    const bool live = (mask >> (16 * r + g + 8 * (i >> 1))) & 1u;
+                    s[r][t][i] = live ? s[r][t][i] * qscale : -INFINITY;
+                    mx[t][i & 1] = fmaxf(mx[t][i & 1], s[r][t][i]);
                 }
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 1));
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 2));
-            move |= mx[i] > m[i] + kRescale;
+            move |= mx[t][0] > m[t][0] + kRescale || mx[t][1] > m[t][1] + kRescale;
         }
         if (__any_sync(kFull, move)) {
 #pragma unroll
-            for (int i = 0; i < RB; ++i) {
-                const float mn = fmaxf(m[i], mx[i]);
-                const float a = mn == -INFINITY ? 1.f : exp2f(m[i] - mn);
-                m[i] = mn;
-                l[i] *= a;
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    o[j][2 * i] *= a;
-                    o[j][2 * i + 1] *= a;
-                    if (RB == 1) {  // the low parts' rows belong to the same head
-                        o[j][2] *= a;
-                        o[j][3] *= a;
+                for (int i = 0; i < 2; ++i) {
+                    float x = mx[t][i];
+                    x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+                    const float mn = fmaxf(m[t][i], x);
+                    const float a = mn == -INFINITY ? 1.f : exp2f(m[t][i] - mn);
+                    m[t][i] = mn;
+                    l[t][i] *= a;
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        o[j][t][i] *= a;
+                        o[j][t][i + 2] *= a;
+                    }
+                }
+        }
+#pragma unroll
+        for (int r = 0; r < KT / 16; ++r) {
+            uint32_t hi[NT][2], lo[NT][2];  // P^T: keys 0..7 and 8..15 of the 16
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float p0 = ex2_approx(s[r][t][2 * i] - m0), p1 = ex2_approx(s[r][t][2 * i + 1] - m1);
+                    l[t][0] += p0;
+                    l[t][1] += p1;
+                    const unsigned u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+                    const uint32_t h = __byte_perm(u0, u1, 0x7632);
+                    const uint32_t w = pack_bf16(fmaxf(p0 - __uint_as_float(u0 & 0xffff0000u), kTiny),
+                                                 fmaxf(p1 - __uint_as_float(u1 & 0xffff0000u), kTiny));
+                    if constexpr (kTwin) {
+                        hi[t][i] = transpose8(c < 2 ? h : w);
+                    } else {
+                        hi[t][i] = transpose8(h);
+                        lo[t][i] = transpose8(w);
                     }
                 }
             }
-        }
-        uint32_t hi[KT / 8][2], lo[KT / 8][2];  // P: column pair of row block 0 and 1
-#pragma unroll
-        for (int i = 0; i < RB; ++i) {
-            const float mu = m[i] == -INFINITY ? 0.f : m[i];
-#pragma unroll
-            for (int j = 0; j < KT / 8; ++j) {
-                const float p0 = ex2_approx(s[j][2 * i] - mu), p1 = ex2_approx(s[j][2 * i + 1] - mu);
-                l[i] += p0 + p1;
-                const unsigned u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
-                hi[j][i] = __byte_perm(u0, u1, 0x7632);
-                lo[j][i] = pack_bf16(fmaxf(p0 - __uint_as_float(u0 & 0xffff0000u), kTiny),
-                                     fmaxf(p1 - __uint_as_float(u1 & 0xffff0000u), kTiny));
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < KT / 16; ++k) {
-            uint32_t pa[4], pl[4];
-            if constexpr (RB == 1) {
-                pa[0] = hi[2 * k][0];
-                pa[1] = lo[2 * k][0];
-                pa[2] = hi[2 * k + 1][0];
-                pa[3] = lo[2 * k + 1][0];
-            } else {
-                pa[0] = hi[2 * k][0];
-                pa[1] = hi[2 * k][1];
-                pa[2] = hi[2 * k + 1][0];
-                pa[3] = hi[2 * k + 1][1];
-                pl[0] = lo[2 * k][0];
-                pl[1] = lo[2 * k][1];
-                pl[2] = lo[2 * k + 1][0];
-                pl[3] = lo[2 * k + 1][1];
-            }
-            const int key = 16 * k + ((lane >> 3) & 1) * 8 + (lane & 7);
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
-                uint32_t b[4];
-                ldsm4_t(vbuf + ring_off<RowBytes>(key, 2 * j + (lane >> 4)), b);
-                mma16816(o[2 * j], pa, b[0], b[1]);
-                mma16816(o[2 * j + 1], pa, b[2], b[3]);
-                if constexpr (RB == 2) {
-                    mma16816(o[2 * j], pl, b[0], b[1]);
-                    mma16816(o[2 * j + 1], pl, b[2], b[3]);
+                uint32_t a[4];
+                ldsm4_t(vbuf + ring_off<RowBytes>(16 * r + (lane >> 4) * 8 + (lane & 7), 2 * j + ((lane >> 3) & 1)), a);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    mma16816(o[j][t], a, hi[t][0], hi[t][1]);
+                    if constexpr (!kTwin) mma16816(o[j][t], a, lo[t][0], lo[t][1]);
                 }
             }
         }
@@ -212,38 +237,38 @@ struct MmaTile {
     __device__ __forceinline__ void put(float* slot, bool add, int lane) {
         const int g = lane >> 2, c = lane & 3;
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-            float sum = l[i];
-            sum += __shfl_xor_sync(kFull, sum, 1);
-            sum += __shfl_xor_sync(kFull, sum, 2);
-            const int h = g + 8 * i;
-            float a = 1.f, b = 0.f, mn = m[i];
-            if (add && h < G) {
-                const float ms = slot[G * D + h];
-                mn = fmaxf(m[i], ms);
-                a = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mn);
-                b = ms == -INFINITY ? 0.f : exp2f(ms - mn);
-                sum = a * sum + b * slot[G * D + G + h];
-            }
-            __syncwarp();
-            if (h < G) {
-                if (c == 0) {
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int h = 8 * t + 2 * c + i;
+                const bool mine = h < G && (!kTwin || c < 2);
+                float sum = l[t][i];
+                sum += __shfl_xor_sync(kFull, sum, 4);
+                sum += __shfl_xor_sync(kFull, sum, 8);
+                sum += __shfl_xor_sync(kFull, sum, 16);
+                float a = 1.f, b = 0.f, mn = m[t][i];
+                if (add && mine) {
+                    const float ms = slot[G * D + h];
+                    mn = fmaxf(mn, ms);
+                    a = m[t][i] == -INFINITY ? 0.f : exp2f(m[t][i] - mn);
+                    b = ms == -INFINITY ? 0.f : exp2f(ms - mn);
+                    sum = a * sum + b * slot[G * D + G + h];
+                }
+                __syncwarp();
+                if (mine && g == 0) {
                     slot[G * D + h] = mn;
                     slot[G * D + G + h] = sum;
                 }
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    float x0 = o[j][2 * i], x1 = o[j][2 * i + 1];
-                    if (RB == 1) {
-                        x0 += o[j][2];
-                        x1 += o[j][3];
+                for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = o[j][t][i + 2 * e];
+                        if (kTwin) x += __shfl_xor_sync(kFull, x, 2);  // the low parts' column
+                        float* p = slot + h * D + 16 * j + 8 * e + g;
+                        if (mine) *p = add ? a * x + b * *p : x;
                     }
-                    float* p = slot + h * D + 8 * j + 2 * c;
-                    p[0] = add ? a * x0 + b * p[0] : x0;
-                    p[1] = add ? a * x1 + b * p[1] : x1;
-                }
             }
-        }
     }
 };
 
@@ -267,6 +292,8 @@ struct FmaTile {
     float q[G][4], o[G][4];
     float m, l;  // of head lane % G (G <= 16 lanes hold it several times over; l is a share)
 
+    __device__ __forceinline__ void fetch_q(const T*, int) {}
+    __device__ __forceinline__ void take_q(const T* src, float qscale, int lane) { load_q(src, qscale, lane); }
     __device__ __forceinline__ void load_q(const T* src, float qscale, int lane) {
         const int e = (lane % LR) * 4;
 #pragma unroll
@@ -415,46 +442,50 @@ struct FmaTile {
 // ---- the list of tiles ------------------------------------------------------------------
 
 struct Share {
-    int64_t unit0;     // first tile of the unit at x (in the list)
-    int b, h, t;       // sequence (-1: none), KV head and tile inside the unit at x
+    int64_t pos0;      // position of the unit's first tile in the list
+    int b, h, t;       // sequence (-1: none), KV head and tile inside the unit (< 0: in front of its tiles)
     int n, nt;         // keys and tiles of sequence b
 };
 
 __device__ __forceinline__ int keys_of(const PagedParams& p, int b) { return min(max(p.len[b], 0), p.N); }
 
-__device__ __forceinline__ int64_t total_tiles(const PagedParams& p, int tk, int lane) {
+// positions a unit takes
+__device__ __forceinline__ int span(int n, int tk) { return n > 0 ? (n + tk - 1) / tk + kUnitCost : 0; }
+
+__device__ __forceinline__ int64_t list_length(const PagedParams& p, int tk, int lane) {
     int64_t sum = 0;
-    for (int b = lane; b < p.B; b += 32) sum += (keys_of(p, b) + tk - 1) / tk;
+    for (int b = lane; b < p.B; b += 32) sum += span(keys_of(p, b), tk);
 #pragma unroll
     for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(kFull, sum, w);
     return sum * p.Hkv;
 }
 
-// where tile x (< total) of the list lies; called by whole warps
+// where position x of the list lies; called by whole warps
 __device__ __forceinline__ void locate(const PagedParams& p, int tk, int64_t x, int lane, Share& s) {
     s.b = -1;
-    int64_t base = 0;  // tiles (of one head) before this round of 32 sequences
+    int64_t base = 0;  // positions (of one head) before this round of 32 sequences
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
         const int n = b < p.B ? keys_of(p, b) : 0;
-        const int nt = (n + tk - 1) / tk;
-        int64_t end = nt;
+        const int len = span(n, tk);
+        int64_t end = len;
 #pragma unroll
         for (int w = 1; w < 32; w <<= 1) {
             const int64_t y = __shfl_up_sync(kFull, end, w);
             if (lane >= w) end += y;
         }
-        const int64_t first = (base + end - nt) * p.Hkv;
-        const unsigned hit = __ballot_sync(kFull, nt > 0 && x >= first && x < (base + end) * p.Hkv);
+        const int64_t first = (base + end - len) * p.Hkv;
+        const unsigned hit = __ballot_sync(kFull, len > 0 && x >= first && x < (base + end) * p.Hkv);
         if (hit) {
             const int at = __ffs(hit) - 1;
             const int64_t f = __shfl_sync(kFull, first, at);
+            const int one = __shfl_sync(kFull, len, at);
             s.b = b0 + at;
             s.n = __shfl_sync(kFull, n, at);
-            s.nt = __shfl_sync(kFull, nt, at);
-            s.h = (int)((x - f) / s.nt);
-            s.t = (int)((x - f) % s.nt);
-            s.unit0 = f + (int64_t)s.h * s.nt;
+            s.nt = one - kUnitCost;
+            s.h = (int)((x - f) / one);
+            s.pos0 = f + (int64_t)s.h * one + kUnitCost;
+            s.t = (int)(x - s.pos0);
             return;
         }
         base += __shfl_sync(kFull, end, 31);
@@ -467,7 +498,7 @@ __device__ __forceinline__ int next_seq(const PagedParams& p, int b, int& n) {
     return b;
 }
 
-// share c of `shares` (at most the number of tiles, so that none is empty)
+// first position of share c of `shares` (at most `total`, so that none is empty)
 __device__ __forceinline__ int64_t share_begin(int64_t total, int64_t c, int64_t shares) { return total * c / shares; }
 
 template <class Tile>
@@ -503,18 +534,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
             if (lse)
                 for (int i = tid; i < p.Hq; i += kWarps * 32) lse[(size_t)b * p.Hq + i] = -INFINITY;
         }
-    const int64_t total = total_tiles(p, TK, lane);
+    const int64_t total = list_length(p, TK, lane);
     const int64_t shares = min((int64_t)grid, total);
     if (cta >= shares) return;
     const int64_t x0 = share_begin(total, cta, shares), x1 = share_begin(total, cta + 1, shares);
     Share at;
     locate(p, TK, x0, lane, at);
-    if (at.b < 0) return;
+    at.t = max(at.t, 0);
+    if (at.b < 0 || at.pos0 + at.t >= x1) return;
 
     // ---- the loading side: its own place in the list, kStages - 1 tiles ahead
     int lb = at.b, lh = at.h, lt = at.t, ln = at.n, lnt = at.nt;
-    int64_t left = x1 - x0;  // tiles not yet issued
-    int page = -1;           // of this lane's row of the next tile (lanes < KT)
+    int64_t left = x1 - (at.pos0 + at.t);  // positions up to the share's end
+    int page = -1;                         // of this lane's row of the next tile (lanes < KT)
     auto fetch = [&]() {
         const int pos = lt * TK + warp * KT + lane;
         page = left > 0 && lane < KT && pos < ln ? __ldg(p.table + (size_t)lb * p.W + pos / p.S) : -1;
@@ -550,6 +582,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
             --left;
             if (++lt == lnt) {
                 lt = 0;
+                left -= kUnitCost;
                 if (++lh == p.Hkv) {
                     lh = 0;
                     lb = next_seq(p, lb + 1, ln);
@@ -569,9 +602,20 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
     Tile tile;
     tile.reset();
     int b = at.b, h = at.h, t = at.t, n = at.n, nt = at.nt, t_first = at.t;
-    tile.load_q(q + ((size_t)b * p.Hq + (size_t)h * G) * D, p.qscale, lane);
+    auto query = [&](int bb, int hh) { return q + ((size_t)bb * p.Hq + (size_t)hh * G) * D; };
+    tile.load_q(query(b, h), p.qscale, lane);
     int stage = 0, fill = kStages - 1;
-    for (int64_t x = x0; x < x1; ++x) {
+    for (int64_t x = at.pos0 + at.t;; ++x) {
+        // the unit that follows, if it is this share's: its queries are fetched behind the last tile
+        const bool next = t + 1 == nt && x + 1 + kUnitCost < x1;
+        int b2 = b, h2 = h, n2 = n;
+        if (next) {
+            if (++h2 == p.Hkv) {
+                h2 = 0;
+                b2 = min(next_seq(p, b + 1, n2), p.B - 1);  // positions are left, so there is one
+            }
+            tile.fetch_q(query(b2, h2), lane);
+        }
         tc::cp_async_wait_group<kStages - 2>();
         __syncwarp();
         const unsigned mask = sm.mask[warp][stage];
@@ -585,6 +629,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
         if (t < nt && x + 1 < x1) continue;
         // the unit, or this CTA's part of it, is through: merge the warps
         const bool whole = t_first == 0 && t == nt;
+        __syncthreads();  // the slots' last contents have been read
         constexpr int NS = Smem<Tile>::kSlots;
 #pragma unroll
         for (int r = 0; r < kWarps / NS; ++r) {
@@ -628,17 +673,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
                 }
             }
         }
-        __syncthreads();
-        if (x + 1 >= x1) break;
+        if (!next) break;
         tile.reset();
+        tile.take_q(query(b2, h2), p.qscale, lane);
+        b = b2;
+        h = h2;
+        n = n2;
+        nt = (n + TK - 1) / TK;
         t = t_first = 0;
-        if (++h == p.Hkv) {
-            h = 0;
-            b = next_seq(p, b + 1, n);
-            if (b == p.B) break;
-            nt = (n + TK - 1) / TK;
-        }
-        tile.load_q(q + ((size_t)b * p.Hq + (size_t)h * G) * D, p.qscale, lane);
+        x += kUnitCost;
     }
     tc::cp_async_wait_all();
 }
@@ -655,13 +698,13 @@ __global__ void __launch_bounds__(128) paged_join_kernel(T* __restrict__ out, fl
     const int64_t grid = gridDim.x, c = blockIdx.x;
     const int hh = blockIdx.y;
     if (c == 0) return;
-    const int64_t total = total_tiles(p, tk, lane);
+    const int64_t total = list_length(p, tk, lane);
     const int64_t shares = min(grid, total);
     if (c >= shares) return;
     Share at;
     locate(p, tk, share_begin(total, c, shares), lane, at);
-    if (at.b < 0 || at.t == 0 || share_begin(total, c - 1, shares) > at.unit0) return;
-    const int64_t end = at.unit0 + at.nt;
+    if (at.b < 0 || at.t <= 0 || share_begin(total, c - 1, shares) > at.pos0) return;
+    const int64_t end = at.pos0 + at.nt;
     // c - 1 and c, then every share that begins before the unit's end: the last such
     // share is the one that holds tile end - 1
     const int parts = (int)((end * shares - 1) / total - (c - 1)) + 1;
@@ -714,7 +757,7 @@ cudaError_t launch_tile(const void* q, const void* k_new, const void* v_new, voi
     const int smem = (int)sizeof(Smem<Tile>);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int64_t per_unit = ((int64_t)p.N + TK - 1) / TK, most = (int64_t)p.B * p.Hkv * per_unit;
+    const int64_t per_unit = ((int64_t)p.N + TK - 1) / TK, most = (int64_t)p.B * p.Hkv * (per_unit + kUnitCost);
     int64_t grid = 2 * (int64_t)sms;  // two CTAs an SM, all resident at once
     if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
     if (grid > most) grid = most;

@@ -2,6 +2,7 @@
 // the attention, the page state's layout and the address of a token's row.
 #pragma once
 
+#include <atomic>
 #include <stdint.h>
 
 #include "pisa_device.cuh"
@@ -9,6 +10,19 @@
 namespace pisa {
 
 constexpr float kLn2 = 0.69314718055994531f;
+
+// SMs of the current device (a fixed fact of it, looked up once)
+inline int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    int sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (sms == 0) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+        if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+    }
+    return sms;
+}
 
 // The attention's workspace holds two parts for each of at most this many CTAs.
 constexpr int kPagedMaxCtas = 512;

@@ -438,7 +438,7 @@ def pages_width(cfg, pages) -> int:
 
 
 def pisa_pages_state_words(pages) -> int:
-    r = int(load().pisa_pages_state_words(ctypes.byref(pages)))
+    r = int((_lib or load()).pisa_pages_state_words(ctypes.byref(pages)))
     if r < 0:
         _check("pisa_pages_state_words", r)
     return r
@@ -452,35 +452,38 @@ def _pool(cfg, pages):
     return pages.P * cfg.Hkv * pages.S * cfg.d
 
 
+def _refuse(name, t, dtype, n, dev):
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensors on different devices ({dev}, {t.get_device()})")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    raise ValueError(f"{name}: expected at least {n} elements of {dtype}, got {t.numel()} of {t.dtype}")
+
+
 def _paged(name: str, cfg, pages, *args) -> None:
     """Call `name` with tensors given as (tensor, dtype, least number of elements) and
     plain numbers as they are, on the tensors' device and its current stream."""
-    dev, out = None, []
+    dev, out = -1, []
     for a in args:
-        if type(a) is not tuple:
-            out.append(a)
-            continue
-        t, dtype, n = a
-        if t is None:
-            out.append(None)
-            continue
-        if dev is None:
-            dev = t.device
-            if dev.type != "cuda":
-                raise ValueError("tensors must live on a CUDA device")
-        elif t.device != dev:
-            raise ValueError(f"{name}: tensors on different devices ({dev}, {t.device})")
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-        if t.dtype is not dtype or t.numel() < n:
-            raise ValueError(f"{name}: expected at least {n} elements of {dtype}, got {t.numel()} of {t.dtype}")
-        out.append(t.data_ptr())
-    fn = getattr(load(), name)
-    if dev.index == torch.cuda.current_device():
-        status = fn(cfg, pages, *out, torch.cuda.current_stream().cuda_stream)
+        if type(a) is tuple:
+            t, dtype, n = a
+            if t is None:
+                a = None
+            else:
+                if dev < 0:
+                    dev = t.get_device()
+                if t.get_device() != dev or dev < 0 or t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+                    _refuse(name, t, dtype, n, dev)
+                a = t.data_ptr()
+        out.append(a)
+    fn = getattr(_lib or load(), name)
+    if dev == torch._C._cuda_getDevice():
+        status = fn(cfg, pages, *out, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(cfg, pages, *out, torch.cuda.current_stream().cuda_stream)
+            status = fn(cfg, pages, *out, torch._C._cuda_getCurrentRawStream(dev))
     if status != 0:
         _check(name, status)
 

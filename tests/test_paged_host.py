@@ -136,7 +136,10 @@ def test_binding_checks_its_tensors(lib):
         pisa.pisa_pages_init(cfg, pages, i32, i32, i32)
 
     class Fake:   # a CUDA tensor as far as the checks see
-        device = torch.device("cuda", 0)
+        is_cuda, at = True, 0
+
+        def get_device(self):
+            return self.at
 
         def __init__(self, dtype, n, contiguous=True):
             self.dtype, self.n, self.contiguous = dtype, n, contiguous
@@ -149,7 +152,7 @@ def test_binding_checks_its_tensors(lib):
 
     ok = Fake(torch.int32, 1000)
     other = Fake(torch.int32, 1000)
-    other.device = torch.device("cuda", 1)
+    other.at = 1
     with pytest.raises(ValueError, match="elements"):
         pisa._paged("pisa_pages_init", cfg, pages, (Fake(torch.int64, 1000), torch.int32, 10))
     with pytest.raises(ValueError, match="elements"):
