@@ -12,12 +12,22 @@
 // the workspace, which paged_join_kernel joins in share order (the result
 // depends on the lengths alone, not on timing).
 //
+// Few and short units (see launch_tile) go without list and join: a cluster of up
+// to 8 CTAs takes one unit and joins its parts through its shared memory.
+//
 // Inside a CTA each of the 4 warps takes KT keys of a tile and streams them
-// through a ring of its own (cp.async, kStages x 8 KB), with no barrier
-// before the unit ends: a warp that waits for memory holds up no other.
+// through a ring of its own (kStages x 8 KB), with no barrier before the unit ends: a
+// warp that waits for memory holds up no other. The rows come by TMA where a page
+// holds whole groups of KT rows, else by cp.async, which takes any page size (and
+// starts sooner: the clusters use it).
+#include <cooperative_groups.h>
+#include <cuda.h>  // CUtensorMap
+
 #include "pisa_internal.h"
 #include "pisa_paged.cuh"
 #include "tc.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace pisa {
 
@@ -27,6 +37,7 @@ constexpr int kWarps = 4;
 constexpr int kStages = 3;
 constexpr int kStageBytes = 8192;  // KT key rows, then KT value rows
 constexpr int kUnitCost = 1;  // 0: 104 us, 1: 77.6, 2: 78.9, 4: 83.1 for 64 sequences of 0..15 K tokens, 32 / 8 heads
+constexpr int kClusterTiles = 4;   // tiles a CTA of a cluster may have to take
 constexpr float kRescale = 8.f;    // see softmax below
 constexpr float kTiny = 1.17549435e-38f;  // smallest normal number
 
@@ -64,11 +75,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// byte offset of 16-byte chunk c of row r: chunks are XOR-swizzled by the row
-// so that the 8 rows of one ldmatrix phase hit distinct banks
-template <int RowBytes>
+// Byte offset of 16-byte chunk c of row r of a stage's keys (or values): runs of 128 bytes
+// of all rows one after another, chunks XOR-swizzled by the row so that the 8 rows of
+// one ldmatrix phase hit distinct banks (TMA's 128-byte swizzle; stages are 1 KB aligned).
+template <int Rows>
 __device__ __forceinline__ uint32_t ring_off(int r, int c) {
-    return (uint32_t)(r * RowBytes + ((c ^ (r & 7)) << 4));
+    return (uint32_t)((c >> 3) * Rows * 128 + r * 128 + (((c ^ r) & 7) << 4));
+}
+
+// rows [y, y + box) x 128 bytes from x (elements) of a pool into shared memory
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(y), "r"(tc::smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(tc::smem_u32(bar)), "r"(bytes)
+                 : "memory");
 }
 
 // ---- one warp's tile, bf16: tensor cores -------------------------------------------
@@ -155,7 +180,7 @@ struct MmaTile {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 uint32_t a[4];
-                ldsm4(kbuf + ring_off<RowBytes>(16 * r + (lane & 15), 2 * k + (lane >> 4)), a);
+                ldsm4(kbuf + ring_off<KT>(16 * r + (lane & 15), 2 * k + (lane >> 4)), a);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) mma16816(s[r][t], a, qb[k][t][0], qb[k][t][1]);
             }
@@ -224,7 +249,7 @@ struct MmaTile {
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
                 uint32_t a[4];
-                ldsm4_t(vbuf + ring_off<RowBytes>(16 * r + (lane >> 4) * 8 + (lane & 7), 2 * j + ((lane >> 3) & 1)), a);
+                ldsm4_t(vbuf + ring_off<KT>(16 * r + (lane >> 4) * 8 + (lane & 7), 2 * j + ((lane >> 3) & 1)), a);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     mma16816(o[j][t], a, hi[t][0], hi[t][1]);
@@ -232,6 +257,10 @@ struct MmaTile {
                 }
             }
         }
+    }
+    __device__ __forceinline__ void poison() {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) l[t][0] = l[t][1] = NAN;
     }
     // this warp's state into a merge slot ([G][D] o, then m[G], l[G]); `add`: merged with what is there
     __device__ __forceinline__ void put(float* slot, bool add, int lane) {
@@ -317,7 +346,7 @@ struct FmaTile {
         float4 v;
         asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];\n"
                      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                     : "r"(buf + ring_off<RowBytes>(r, c))
+                     : "r"(buf + ring_off<KT>(r, c))
                      : "memory");
         return v;
     }
@@ -408,6 +437,7 @@ struct FmaTile {
         }
         __syncwarp();  // scratch is rewritten by the next tile
     }
+    __device__ __forceinline__ void poison() { l = NAN; }
     __device__ __forceinline__ void put(float* slot, bool add, int lane) {
         float sum = l;
 #pragma unroll
@@ -507,78 +537,141 @@ struct Smem {
     // merge slots: one a warp where they fit beside the ring twice an SM, else warps take turns
     static constexpr int kRoom = 115712 - kWarps * kStages * kStageBytes - kWarps * (Tile::kScratchFloats + 1) * 4 - 256;
     static constexpr int kSlots = 4 * kSlotFloats * 4 <= kRoom ? 4 : 2 * kSlotFloats * 4 <= kRoom ? 2 : 1;
-    alignas(128) uint8_t ring[kWarps][kStages][kStageBytes];
+    alignas(1024) uint8_t ring[kWarps][kStages][kStageBytes];
     float slot[kSlots][kSlotFloats];
     float scratch[kWarps][Tile::kScratchFloats + 1];
     unsigned mask[kWarps][kStages];
+    uint64_t full[kWarps][kStages];  // TMA: a stage's rows have landed
+    // a cluster's CTA: its part of the unit ([G][D] o, then m[G], l[G]), over the ring
+    __device__ __forceinline__ float* fin() { return reinterpret_cast<float*>(&ring[0][0][0]); }
 };
 
-template <class Tile>
+// what a kernel is: the list fed by cp.async, a unit a cluster, the list fed by TMA
+enum Mode { kList, kCluster, kListTma };
+
+template <class Tile, Mode MODE>
 __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
     const typename Tile::T* __restrict__ q, const typename Tile::T* __restrict__ k_new,
     const typename Tile::T* __restrict__ v_new, typename Tile::T* __restrict__ K, typename Tile::T* __restrict__ V,
-    typename Tile::T* __restrict__ out, float* __restrict__ lse, float* __restrict__ part, PagedParams p) {
+    typename Tile::T* __restrict__ out, float* __restrict__ lse, float* __restrict__ part, PagedParams p,
+    const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using T = typename Tile::T;
+    constexpr bool CLUSTER = MODE == kCluster, TMA = MODE == kListTma;
     constexpr int D = Tile::D, G = Tile::G, KT = Tile::KT, TK = kWarps * KT;
     constexpr int CPR = Tile::RowBytes / 16, RPI = 32 / CPR;  // chunks a row, rows a warp copies at once
-    extern __shared__ __align__(128) uint8_t raw[];
+    extern __shared__ __align__(1024) uint8_t raw[];
     Smem<Tile>& sm = *reinterpret_cast<Smem<Tile>*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int grid = gridDim.x, cta = blockIdx.x;
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-
-    // empty sequences: nothing to attend to
-    for (int b = cta; b < p.B; b += grid)
-        if (keys_of(p, b) == 0) {
-            for (int i = tid; i < p.Hq * D; i += kWarps * 32) out[(size_t)b * p.Hq * D + i] = (T)0.f;
-            if (lse)
-                for (int i = tid; i < p.Hq; i += kWarps * 32) lse[(size_t)b * p.Hq + i] = -INFINITY;
-        }
-    const int64_t total = list_length(p, TK, lane);
-    const int64_t shares = min((int64_t)grid, total);
-    if (cta >= shares) return;
-    const int64_t x0 = share_begin(total, cta, shares), x1 = share_begin(total, cta + 1, shares);
     Share at;
-    locate(p, TK, x0, lane, at);
-    at.t = max(at.t, 0);
-    if (at.b < 0 || at.pos0 + at.t >= x1) return;
+    int64_t x1;  // the end of this CTA's share
+    if constexpr (CLUSTER) {
+        const int size = (int)cg::this_cluster().num_blocks(), unit = cta / size, rank = cta % size;
+        at.b = unit / p.Hkv;
+        at.h = unit % p.Hkv;
+        at.n = keys_of(p, at.b);
+        at.nt = (at.n + TK - 1) / TK;
+        at.pos0 = 0;
+        at.t = at.nt * rank / size;
+        x1 = at.nt * (rank + 1) / size;
+    } else {
+        asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+        // empty sequences: nothing to attend to
+        for (int b = cta; b < p.B; b += grid)
+            if (keys_of(p, b) == 0) {
+                for (int i = tid; i < p.Hq * D; i += kWarps * 32) out[(size_t)b * p.Hq * D + i] = (T)0.f;
+                if (lse)
+                    for (int i = tid; i < p.Hq; i += kWarps * 32) lse[(size_t)b * p.Hq + i] = -INFINITY;
+            }
+        const int64_t total = list_length(p, TK, lane);
+        const int64_t shares = min((int64_t)grid, total);
+        if (cta >= shares) return;
+        x1 = share_begin(total, cta + 1, shares);
+        locate(p, TK, share_begin(total, cta, shares), lane, at);
+        at.t = max(at.t, 0);
+        if (at.b < 0 || at.pos0 + at.t >= x1) return;
+    }
+
+    if constexpr (TMA) {
+        if (lane == 0) {
+            for (int i = 0; i < kStages; ++i) tc::mbar_init(&sm.full[warp][i], 1);
+            tc::fence_mbar_init();
+        }
+        __syncwarp();  // a warp's barriers are its own
+    }
 
     // ---- the loading side: its own place in the list, kStages - 1 tiles ahead
     int lb = at.b, lh = at.h, lt = at.t, ln = at.n, lnt = at.nt;
     int64_t left = x1 - (at.pos0 + at.t);  // positions up to the share's end
     int page = -1;                         // of this lane's row of the next tile (lanes < KT)
     auto fetch = [&]() {
+        if constexpr (TMA) {  // one page for all rows
+            const int pos = lt * TK + warp * KT;
+            page = left > 0 && pos < ln ? __ldg(p.table + (size_t)lb * p.W + pos / p.S) : -1;
+            return;
+        }
         const int pos = lt * TK + warp * KT + lane;
         page = left > 0 && lane < KT && pos < ln ? __ldg(p.table + (size_t)lb * p.W + pos / p.S) : -1;
     };
+    // the token in hand lies in this warp's rows of tile t of a sequence of n keys
+    auto fresh_at = [&](int t, int n) { return k_new != nullptr && (n - 1) / TK == t && ((n - 1) % TK) / KT == warp; };
+    auto issue_rows = [&](int stage) {
+        const int pos = lt * TK + warp * KT + lane;
+        const bool live = lane < KT && pos < ln && page >= 0 && page < p.P;
+        const int row = live ? (page * p.Hkv + lh) * p.S + pos % p.S : -1;  // of the pool (< 2^31)
+        const unsigned mask = __ballot_sync(kFull, live);
+        if (lane == 0) sm.mask[warp][stage] = mask;
+        const uint32_t kbuf = tc::smem_u32(sm.ring[warp][stage]), vbuf = kbuf + kStageBytes / 2;
+        const int c = lane % CPR;
+        const bool fresh = fresh_at(lt, ln);
+#pragma unroll
+        for (int i = 0; i < KT / RPI; ++i) {
+            const int r = i * RPI + lane / CPR;
+            const int src = __shfl_sync(kFull, row, r);
+            const size_t e = (size_t)max(src, 0) * D + c * (16 / sizeof(T));
+            const T *ks = K + e, *vs = V + e;
+            if (fresh && lt * TK + warp * KT + r == ln - 1) {  // the token in hand: from its rows, and into its page
+                const size_t u = ((size_t)lb * p.Hkv + lh) * D + c * (16 / sizeof(T));
+                ks = k_new + u;
+                vs = v_new + u;
+                if (src >= 0) {
+                    *reinterpret_cast<uint4*>(K + e) = __ldg(reinterpret_cast<const uint4*>(ks));
+                    *reinterpret_cast<uint4*>(V + e) = __ldg(reinterpret_cast<const uint4*>(vs));
+                }
+            }
+            cp_async16_if(kbuf + ring_off<KT>(r, c), ks, src >= 0);
+            cp_async16_if(vbuf + ring_off<KT>(r, c), vs, src >= 0);
+        }
+    };
+    auto issue_tma = [&](int stage) {
+        const int pos = lt * TK + warp * KT;
+        const bool live = pos < ln && (unsigned)page < (unsigned)p.P;
+        const int row = live ? (page * p.Hkv + lh) * p.S + pos % p.S : 0;
+        if (lane == 0) {
+            const int rows = live ? min(KT, ln - pos) : 0;
+            sm.mask[warp][stage] = rows == 32 ? kFull : (1u << rows) - 1u;
+            uint64_t* bar = &sm.full[warp][stage];
+            const uint32_t kbuf = tc::smem_u32(sm.ring[warp][stage]);
+            mbar_expect(bar, live ? kStageBytes : 0);
+            if (live) {
+#pragma unroll
+                for (int i = 0; i < Tile::RowBytes / 128; ++i) {
+                    tma_rows(kbuf + i * KT * 128, &k_map, i * (128 / (int)sizeof(T)), row, bar);
+                    tma_rows(kbuf + kStageBytes / 2 + i * KT * 128, &v_map, i * (128 / (int)sizeof(T)), row, bar);
+                }
+            }
+        }
+        if (live && fresh_at(lt, ln) && lane < CPR) {  // into its page; the ring gets it when the stage is used
+            const size_t u = ((size_t)lb * p.Hkv + lh) * D + lane * (16 / sizeof(T));
+            const size_t e = (size_t)(row + (ln - 1) % KT) * D + lane * (16 / sizeof(T));
+            *reinterpret_cast<uint4*>(K + e) = __ldg(reinterpret_cast<const uint4*>(k_new + u));
+            *reinterpret_cast<uint4*>(V + e) = __ldg(reinterpret_cast<const uint4*>(v_new + u));
+        }
+    };
     auto issue = [&](int stage) {
         if (left > 0) {
-            const int pos = lt * TK + warp * KT + lane;
-            const bool live = lane < KT && pos < ln && page >= 0 && page < p.P;
-            const int row = live ? (page * p.Hkv + lh) * p.S + pos % p.S : -1;  // of the pool (< 2^31)
-            const unsigned mask = __ballot_sync(kFull, live);
-            if (lane == 0) sm.mask[warp][stage] = mask;
-            const uint32_t kbuf = tc::smem_u32(sm.ring[warp][stage]), vbuf = kbuf + kStageBytes / 2;
-            const int c = lane % CPR;
-            const bool fresh = k_new != nullptr && (ln - 1) / TK == lt && ((ln - 1) % TK) / KT == warp;
-#pragma unroll
-            for (int i = 0; i < KT / RPI; ++i) {
-                const int r = i * RPI + lane / CPR;
-                const int src = __shfl_sync(kFull, row, r);
-                const size_t e = (size_t)max(src, 0) * D + c * (16 / sizeof(T));
-                const T *ks = K + e, *vs = V + e;
-                if (fresh && lt * TK + warp * KT + r == ln - 1) {  // the token in hand: from its rows, and into its page
-                    const size_t u = ((size_t)lb * p.Hkv + lh) * D + c * (16 / sizeof(T));
-                    ks = k_new + u;
-                    vs = v_new + u;
-                    if (src >= 0) {
-                        *reinterpret_cast<uint4*>(K + e) = __ldg(reinterpret_cast<const uint4*>(ks));
-                        *reinterpret_cast<uint4*>(V + e) = __ldg(reinterpret_cast<const uint4*>(vs));
-                    }
-                }
-                cp_async16_if(kbuf + ring_off<Tile::RowBytes>(r, c), ks, src >= 0);
-                cp_async16_if(vbuf + ring_off<Tile::RowBytes>(r, c), vs, src >= 0);
-            }
+            if constexpr (TMA) issue_tma(stage);
+            else issue_rows(stage);
             --left;
             if (++lt == lnt) {
                 lt = 0;
@@ -592,7 +685,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
             }
             fetch();
         }
-        tc::cp_async_commit();
+        if constexpr (!TMA) tc::cp_async_commit();
     };
     fetch();
 #pragma unroll
@@ -605,7 +698,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
     auto query = [&](int bb, int hh) { return q + ((size_t)bb * p.Hq + (size_t)hh * G) * D; };
     tile.load_q(query(b, h), p.qscale, lane);
     int stage = 0, fill = kStages - 1;
-    for (int64_t x = at.pos0 + at.t;; ++x) {
+    uint32_t parity = 0;  // TMA: of the round of stages in use
+    bool failed = false;
+    for (int64_t x = at.pos0 + at.t; x < x1; ++x) {
         // the unit that follows, if it is this share's: its queries are fetched behind the last tile
         const bool next = t + 1 == nt && x + 1 + kUnitCost < x1;
         int b2 = b, h2 = h, n2 = n;
@@ -616,14 +711,49 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
             }
             tile.fetch_q(query(b2, h2), lane);
         }
-        tc::cp_async_wait_group<kStages - 2>();
-        __syncwarp();
-        const unsigned mask = sm.mask[warp][stage];
         const uint32_t kbuf = tc::smem_u32(sm.ring[warp][stage]);
-        tile.step(kbuf, kbuf + kStageBytes / 2, mask, p.qscale, lane, sm.scratch[warp]);
+        if constexpr (TMA) {
+            const bool gave_up = !failed && !tc::mbar_wait(&sm.full[warp][stage], parity, nullptr, 0);
+            if (__any_sync(kFull, gave_up)) {  // after about a second: no more copies, and those under way
+                failed = true;                 // get as long again
+                left = 0;
+                for (int i = 0; i < kStages; ++i)
+                    tc::mbar_wait(&sm.full[warp][(stage + i) % kStages], parity ^ (stage + i >= kStages), nullptr, 0);
+            }
+            const unsigned mask = sm.mask[warp][stage];
+            if (failed) {
+                tile.poison();  // the result is NaN
+            } else if (mask != 0) {
+                const int rows = __popc(mask);
+                const bool fresh = fresh_at(t, n);
+                if (rows < KT || fresh) {
+                    // rows past the end may hold anything: their values count as zeros. The token in hand
+                    // comes from its rows (its page may have been read before they were there).
+                    for (int i = lane; i < (KT - rows) * CPR; i += 32)
+                        *reinterpret_cast<uint4*>(sm.ring[warp][stage] + kStageBytes / 2 + ring_off<KT>(rows + i / CPR, i % CPR)) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    if (fresh && lane < CPR) {
+                        const size_t u = ((size_t)b * p.Hkv + h) * D + lane * (16 / sizeof(T));
+                        uint8_t* at_row = sm.ring[warp][stage] + ring_off<KT>((n - 1) % KT, lane);
+                        *reinterpret_cast<uint4*>(at_row) = __ldg(reinterpret_cast<const uint4*>(k_new + u));
+                        *reinterpret_cast<uint4*>(at_row + kStageBytes / 2) = __ldg(reinterpret_cast<const uint4*>(v_new + u));
+                    }
+                    tc::fence_async_smem();  // before the next TMA write of this stage
+                    __syncwarp();
+                }
+                tile.step(kbuf, kbuf + kStageBytes / 2, mask, p.qscale, lane, sm.scratch[warp]);
+            }
+        } else {
+            tc::cp_async_wait_group<kStages - 2>();
+            __syncwarp();
+            tile.step(kbuf, kbuf + kStageBytes / 2, sm.mask[warp][stage], p.qscale, lane, sm.scratch[warp]);
+        }
         __syncwarp();
         issue(fill);
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+        if (++stage == kStages) {
+            stage = 0;
+            parity ^= 1;
+        }
         fill = fill + 1 == kStages ? 0 : fill + 1;
         ++t;
         if (t < nt && x + 1 < x1) continue;
@@ -657,7 +787,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
                 acc.z += a * x4[2];
                 acc.w += a * x4[3];
             }
-            if (whole) {
+            if constexpr (CLUSTER) {  // this CTA's part, in the ring (all its loads have been used)
+                *reinterpret_cast<float4*>(&sm.fin()[hh * D + e]) = acc;
+                if (e == 0) {
+                    sm.fin()[G * D + hh] = M;
+                    sm.fin()[G * D + G + hh] = sum;
+                }
+            } else if (whole) {
                 const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;  // no key counted: 0
                 const float r[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
                 store_vec<T, 4>(out + (unit + hh) * D + e, r);
@@ -684,6 +820,35 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
         x += kUnitCost;
     }
     tc::cp_async_wait_all();
+    if constexpr (CLUSTER) {
+        if (at.t == x1)  // more CTAs than tiles: no part
+            for (int i = tid; i < G * (D + 2); i += kWarps * 32) sm.fin()[i] = i / G == D ? -INFINITY : 0.f;
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        const int size = (int)cluster.num_blocks(), rank = cta % size;
+        const size_t unit = (size_t)at.b * p.Hq + (size_t)at.h * G;
+        for (int i = rank * kWarps * 32 + tid; i < G * D / 4; i += size * kWarps * 32) {
+            const int hh = i / (D / 4), e = (i % (D / 4)) * 4;
+            float M = -INFINITY, sum = 0.f;
+            for (int r = 0; r < size; ++r) M = fmaxf(M, cluster.map_shared_rank(sm.fin(), r)[G * D + hh]);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int r = 0; r < size; ++r) {
+                const float* f = cluster.map_shared_rank(sm.fin(), r);
+                const float m = f[G * D + hh], a = m == -INFINITY ? 0.f : exp2f(m - M);
+                const float4 v = *reinterpret_cast<const float4*>(f + hh * D + e);
+                sum += a * f[G * D + G + hh];
+                acc.x += a * v.x;
+                acc.y += a * v.y;
+                acc.z += a * v.z;
+                acc.w += a * v.w;
+            }
+            const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+            const float r4[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+            store_vec<T, 4>(out + (unit + hh) * D + e, r4);
+            if (lse && e == 0) lse[unit + hh] = (M + log2f(sum)) * kLn2;
+        }
+        cluster.sync();  // the others have read this CTA's part
+    }
 }
 
 // Joins the parts of the units that more than one CTA had a share of. CTA
@@ -748,21 +913,91 @@ __global__ void __launch_bounds__(128) paged_join_kernel(T* __restrict__ out, fl
     }
 }
 
+using PFN_encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// shared memory above 48 KB: asked for once a device and kernel
+template <class Kern>
+cudaError_t allow_smem(Kern kern, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) >> dev) & 1)) return e;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+    return e;
+}
+
+// TMA's view of a pool: all rows of all pages, in boxes of `rows` x 128 bytes
+bool row_map(CUtensorMap* map, const void* pool, const PagedParams& p, int rows, int d, int elem) {
+    static const PFN_encode encode = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+        return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_encode>(fn) : nullptr;
+    }();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)p.P * p.Hkv * p.S};
+    const cuuint64_t strides[1] = {(cuuint64_t)d * elem};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / elem), (cuuint32_t)rows}, step[2] = {1, 1};
+    return encode(map, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                  const_cast<void*>(pool), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <class Tile>
 cudaError_t launch_tile(const void* q, const void* k_new, const void* v_new, void* K, void* V, void* o, float* lse,
                         float* part, const PagedParams& p, int sms, cudaStream_t st) {
     using T = typename Tile::T;
-    constexpr int TK = kWarps * Tile::KT;
-    auto kern = paged_attn_kernel<Tile>;
+    constexpr int TK = kWarps * Tile::KT, D = Tile::D;
     const int smem = (int)sizeof(Smem<Tile>);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    const int64_t per_unit = ((int64_t)p.N + TK - 1) / TK, most = (int64_t)p.B * p.Hkv * (per_unit + kUnitCost);
-    int64_t grid = 2 * (int64_t)sms;  // two CTAs an SM, all resident at once
-    if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
-    if (grid > most) grid = most;
-    kern<<<(unsigned)grid, kWarps * 32, smem, st>>>((const T*)q, (const T*)k_new, (const T*)v_new, (T*)K, (T*)V, (T*)o,
-                                                    lse, part, p);
+    const int64_t per_unit = ((int64_t)p.N + TK - 1) / TK, units = (int64_t)p.B * p.Hkv;
+    const int64_t room = 2 * (int64_t)sms < kPagedMaxCtas ? 2 * (int64_t)sms : kPagedMaxCtas;  // two CTAs an SM
+
+    // One cluster a unit: saves the look at all lengths and the second launch, but
+    // gives a unit at most 8 CTAs, whatever its length.
+    int size = 8;
+    while (size > 1 && units * size > room) size /= 2;
+    if (units <= room && per_unit <= (int64_t)size * kClusterTiles) {
+        static std::atomic<uint64_t> done{0};
+        auto kern = paged_attn_kernel<Tile, kCluster>;
+        const cudaError_t e = allow_smem(kern, smem, done);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(units * size));
+        cfg.blockDim = dim3(kWarps * 32);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = size;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kern, (const T*)q, (const T*)k_new, (const T*)v_new, (T*)K, (T*)V, (T*)o, lse,
+                                  part, p, CUtensorMap{}, CUtensorMap{});
+    }
+
+    int64_t grid = units * (per_unit + kUnitCost);
+    if (grid > room) grid = room;  // all resident at once
+    cudaError_t e;
+    CUtensorMap k_map{}, v_map{};
+    if (p.S % Tile::KT == 0 && row_map(&k_map, K, p, Tile::KT, D, sizeof(T)) && row_map(&v_map, V, p, Tile::KT, D, sizeof(T))) {
+        static std::atomic<uint64_t> done{0};
+        auto kern = paged_attn_kernel<Tile, kListTma>;
+        e = allow_smem(kern, smem, done);
+        if (e != cudaSuccess) return e;
+        kern<<<(unsigned)grid, kWarps * 32, smem, st>>>((const T*)q, (const T*)k_new, (const T*)v_new, (T*)K, (T*)V, (T*)o,
+                                                        lse, part, p, k_map, v_map);
+    } else {
+        static std::atomic<uint64_t> done{0};
+        auto kern = paged_attn_kernel<Tile, kList>;
+        e = allow_smem(kern, smem, done);
+        if (e != cudaSuccess) return e;
+        kern<<<(unsigned)grid, kWarps * 32, smem, st>>>((const T*)q, (const T*)k_new, (const T*)v_new, (T*)K, (T*)V, (T*)o,
+                                                        lse, part, p, k_map, v_map);
+    }
     e = cudaGetLastError();
     if (e != cudaSuccess || per_unit == 1 || grid == 1) return e;  // no unit can be cut
     cudaLaunchConfig_t cfg = {};

@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(256) pages_init_kernel(int32_t* __restrict__ s
 // sharers in this call copy it when no one else holds it). All or nothing. One
 // CTA: the integers are few (B lengths, P / 8 bytes of bitmap) and one block's
 // barriers are cheaper than a second launch.
+constexpr int kReserveIds = 2048;
 constexpr int kReservePer = kReserveMaxSeqs / 1024;  // sequences a thread
 __global__ void __launch_bounds__(1024) pages_reserve_kernel(const int32_t* __restrict__ add, int32_t* __restrict__ state,
                                                              int32_t* __restrict__ table, int32_t* __restrict__ len,
@@ -70,6 +71,7 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const int32_t* __re
                                                              int B, int N, int S, int P, int W) {
     __shared__ int64_t warp_sums[32];
     __shared__ int s_shared;                         // sequences with a shared partial last page
+    __shared__ int s_ids[kReserveIds];               // the first pages handed out
     extern __shared__ int dyn[];                     // two arrays of that list, then four of the sequences
     int* l_seq = dyn;
     int* l_page = dyn + B;
@@ -82,6 +84,17 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const int32_t* __re
     int32_t* refs = state;
     unsigned* bits = reinterpret_cast<unsigned*>(state + L.bits());
     int32_t* ids = state + L.map();
+    // free pages, counted in order of their ids, a run of words a thread (the bitmap is
+    // padded to 4 words); read first, so that the loads overlap the sequences'
+    const int words = (P + 31) / 32, run = ((words + 1023) / 1024 + 3) / 4 * 4;
+    const int w0 = tid * run, w1 = min(w0 + run, words);
+    uint4 head = make_uint4(0u, 0u, 0u, 0u);
+    if (w0 < w1) head = *reinterpret_cast<const uint4*>(bits + w0);
+    int64_t found = __popc(head.x) + __popc(head.y) + __popc(head.z) + __popc(head.w);
+    for (int w = w0 + 4; w < w1; w += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(bits + w);
+        found += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
+    }
     if (tid == 0) s_shared = 0;
     __syncthreads();
 
@@ -129,13 +142,6 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const int32_t* __re
     int64_t at = block_scan(mine, warp_sums, &all);
     const int64_t total = all & (((int64_t)1 << 48) - 1);
 
-    // free pages, in order of their ids: a run of words a thread
-    const int words = (P + 31) / 32, run = ((words + 1023) / 1024 + 3) / 4 * 4;
-    int64_t found = 0;
-    for (int w = tid * run; w < min((tid + 1) * run, words); w += 4) {
-        const uint4 v = *reinterpret_cast<const uint4*>(bits + w);  // the bitmap is padded to 4 words
-        found += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
-    }
     int64_t spare;
     int64_t rank = block_scan(found, warp_sums, &spare);
     const bool fits = total <= spare;
@@ -146,11 +152,14 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const int32_t* __re
         moves[3] = (int)(spare - (fits ? total : 0));
     }
     if (fits) {
-        for (int w = tid * run; w < min((tid + 1) * run, words) && rank < total; ++w) {
-            unsigned v = bits[w];
+        for (int w = w0; w < w1 && rank < total; ++w) {
+            unsigned v = w == w0 ? head.x : w == w0 + 1 ? head.y : w == w0 + 2 ? head.z : w == w0 + 3 ? head.w : bits[w];
             const unsigned was = v;
             while (v && rank < total) {
-                ids[rank++] = w * 32 + __ffs(v) - 1;
+                const int page = w * 32 + __ffs(v) - 1;
+                if (rank < kReserveIds) s_ids[rank] = page;
+                else ids[rank] = page;
+                ++rank;
                 v &= v - 1;
             }
             if (v != was) bits[w] = v;
@@ -180,7 +189,7 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const int32_t* __re
     for (int b = tid >> 5; b < B; b += 32) {
         const int need = s_need[b], base = s_base[b], t = s_tail[b], first = s_have[b] - (t >= 0 ? 1 : 0);
         for (int k = lane; k < need; k += 32) {
-            const int page = ids[base + k];
+            const int page = base + k < kReserveIds ? s_ids[base + k] : ids[base + k];
             refs[page] = 1;
             table[(size_t)b * W + first + k] = page;
             if (k == 0 && t >= 0) {
@@ -315,9 +324,12 @@ __global__ void __launch_bounds__(256) compact_table_kernel(const int32_t* __res
 }
 
 // Page data of the moves: a page of a pool is one run of bytes, cut into segments
-// of kSegment; a block takes a segment at a time, 4 x 16 bytes a thread in flight.
+// of kSegment; a block takes a segment at a time, 2 x 16 bytes a thread in flight, and
+// far more blocks than fit at once even out the ends (grids of 8, 16, 64 a SM: 164, 149,
+// 143 us for 3600 pages of 128 KB, 6.6 TB/s read and written at best).
 constexpr int kSegment = 16384;
-__global__ void __launch_bounds__(256) pages_copy_kernel(const int32_t* __restrict__ moves, uint8_t* __restrict__ K,
+constexpr int kCopyThreads = 512, kCopyPer = kSegment / 16 / kCopyThreads;
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const int32_t* __restrict__ moves, uint8_t* __restrict__ K,
                                                          uint8_t* __restrict__ V, int64_t page_bytes, int segments, int P,
                                                          int max_moves) {
     const int64_t tasks = (int64_t)min(max(moves[0], 0), max_moves) * 2 * segments;
@@ -331,36 +343,51 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const int32_t* __restri
         const int chunks = (int)(min(page_bytes - off, (int64_t)kSegment) / 16);
         const uint4* from = reinterpret_cast<const uint4*>(pool + (int64_t)src * page_bytes + off);
         uint4* to = reinterpret_cast<uint4*>(pool + (int64_t)dst * page_bytes + off);
-        uint4 v[4];
+        uint4 v[kCopyPer];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (threadIdx.x + i * 256 < chunks) v[i] = from[threadIdx.x + i * 256];
+        for (int i = 0; i < kCopyPer; ++i)
+            if (threadIdx.x + i * kCopyThreads < chunks) v[i] = __ldcs(from + threadIdx.x + i * kCopyThreads);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (threadIdx.x + i * 256 < chunks) to[threadIdx.x + i * 256] = v[i];
+        for (int i = 0; i < kCopyPer; ++i)
+            if (threadIdx.x + i * kCopyThreads < chunks) __stcs(to + threadIdx.x + i * kCopyThreads, v[i]);
     }
 }
 
-// New rows into the pages: 16 bytes of K and of V a thread. Sequence b's rows are
-// one run [Hkv, T, d] of the input; row i < count[b] goes to token len[b] - count[b] + i.
+// New rows into the pages: kAppendPer times 16 bytes of K and of V a thread, all
+// loaded before the first is stored (1, 2, 4 times: 42.1, 42.7, 44.7 us for 4 x 8192 full
+// rows of 8 heads, 54.1, 51.0, 52.5 us with the page calls where half of 32 sequences
+// add 1 to 2 K rows). Sequence b's rows are one run [Hkv, T, d] of the input; row
+// i < count[b] goes to token len[b] - count[b] + i.
+constexpr int kAppendPer = 2;
 __global__ void __launch_bounds__(256) paged_append_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
                                                            const int32_t* __restrict__ count, uint4* __restrict__ K,
                                                            uint4* __restrict__ V, int T, int shift, int64_t per_seq,
                                                            int tiles, PagedParams p) {
     const int b = blockIdx.x / tiles;
-    const int64_t i = (int64_t)(blockIdx.x % tiles) * 256 + threadIdx.x;
-    if (i >= per_seq) return;
+    const int64_t i0 = (int64_t)(blockIdx.x % tiles) * (256 * kAppendPer) + threadIdx.x;
     const int n = p.len[b], m = count[b];
-    const int c = (int)(i & ((1 << shift) - 1));
-    const int64_t row = i >> shift;
-    const int h = (int)(row / T), r = (int)(row % T);
-    if (m < 0 || m > T || n > p.N || m > n || r >= m) return;
-    const int tok = n - m + r, page = p.table[(size_t)b * p.W + tok / p.S];
-    if ((unsigned)page >= (unsigned)p.P) return;
-    const size_t dst = ((((size_t)page * p.Hkv + h) * p.S + tok % p.S) << shift) + c;
-    const size_t src = (size_t)b * per_seq + i;
-    K[dst] = __ldg(k_new + src);
-    V[dst] = __ldg(v_new + src);
+    if (m <= 0 || m > T || n > p.N || m > n) return;
+    uint4 k[kAppendPer], v[kAppendPer];
+    int64_t dst[kAppendPer];
+#pragma unroll
+    for (int u = 0; u < kAppendPer; ++u) {
+        const int64_t i = i0 + u * 256, row = i >> shift;
+        dst[u] = -1;
+        if (i >= per_seq) continue;
+        const int h = (int)(row / T), r = (int)(row % T);
+        if (r >= m) continue;
+        const int tok = n - m + r, page = __ldg(p.table + (size_t)b * p.W + tok / p.S);
+        if ((unsigned)page >= (unsigned)p.P) continue;
+        dst[u] = ((((int64_t)page * p.Hkv + h) * p.S + tok % p.S) << shift) + (i & ((1 << shift) - 1));
+        k[u] = __ldcs(k_new + (size_t)b * per_seq + i);
+        v[u] = __ldcs(v_new + (size_t)b * per_seq + i);
+    }
+#pragma unroll
+    for (int u = 0; u < kAppendPer; ++u)
+        if (dst[u] >= 0) {
+            __stcs(K + dst[u], k[u]);
+            __stcs(V + dst[u], v[u]);
+        }
 }
 
 }  // namespace
@@ -416,8 +443,8 @@ cudaError_t launch_pages_compact(int32_t* state, int32_t* table, int32_t* moves,
 cudaError_t launch_pages_copy(const int32_t* moves, int max_moves, void* K, void* V, int64_t page_bytes, int P, int sms,
                               cudaStream_t st) {
     const int segments = (int)((page_bytes + kSegment - 1) / kSegment);
-    const int64_t want = (int64_t)max_moves * 2 * segments, most = (int64_t)sms * 8;
-    pages_copy_kernel<<<(unsigned)(want < most ? want : most), 256, 0, st>>>(moves, (uint8_t*)K, (uint8_t*)V, page_bytes,
+    const int64_t want = (int64_t)max_moves * 2 * segments, most = (int64_t)sms * 64;
+    pages_copy_kernel<<<(unsigned)(want < most ? want : most), kCopyThreads, 0, st>>>(moves, (uint8_t*)K, (uint8_t*)V, page_bytes,
                                                                              segments, P, max_moves);
     return cudaGetLastError();
 }
@@ -426,7 +453,8 @@ cudaError_t launch_paged_append(int row_bytes, const void* k_new, const void* v_
                                 void* V, const PagedParams& p, cudaStream_t st) {
     int shift = 0;
     while ((16 << shift) < row_bytes) ++shift;  // row_bytes is 128, 256 or 512
-    const int64_t per_seq = ((int64_t)p.Hkv * T) << shift, tiles = (per_seq + 255) / 256;
+    const int64_t per_seq = ((int64_t)p.Hkv * T) << shift, per_block = 256 * kAppendPer,
+                  tiles = (per_seq + per_block - 1) / per_block;
     paged_append_kernel<<<(unsigned)(p.B * tiles), 256, 0, st>>>((const uint4*)k_new, (const uint4*)v_new, count,
                                                                  (uint4*)K, (uint4*)V, T, shift, per_seq, (int)tiles, p);
     return cudaGetLastError();

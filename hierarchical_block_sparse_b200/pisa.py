@@ -437,8 +437,13 @@ def pages_width(cfg, pages) -> int:
     return -(-cfg.N // pages.S)
 
 
+def _state_words(pages):
+    P = pages.P
+    return 2 * (P + 3 & ~3) + 3 * ((P + 31) // 32 + 3 & ~3) + 16
+
+
 def pisa_pages_state_words(pages) -> int:
-    r = int((_lib or load()).pisa_pages_state_words(ctypes.byref(pages)))
+    r = int(load().pisa_pages_state_words(ctypes.byref(pages)))
     if r < 0:
         _check("pisa_pages_state_words", r)
     return r
@@ -472,10 +477,10 @@ def _paged(name: str, cfg, pages, *args) -> None:
             if t is None:
                 a = None
             else:
-                if dev < 0:
-                    dev = t.get_device()
-                if t.get_device() != dev or dev < 0 or t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
-                    _refuse(name, t, dtype, n, dev)
+                d = t.get_device()
+                if d != dev and (dev >= 0 or d < 0) or t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+                    _refuse(name, t, dtype, n, dev if dev >= 0 else d)
+                dev = d
                 a = t.data_ptr()
         out.append(a)
     fn = getattr(_lib or load(), name)
@@ -491,14 +496,14 @@ def _paged(name: str, cfg, pages, *args) -> None:
 def pisa_pages_init(cfg, pages, state, table, lens):
     """An empty cache: every page free, table -1, lengths 0."""
     i32 = torch.int32
-    _paged("pisa_pages_init", cfg, pages, (state, i32, pisa_pages_state_words(pages)),
+    _paged("pisa_pages_init", cfg, pages, (state, i32, _state_words(pages)),
            (table, i32, cfg.B * pages_width(cfg, pages)), (lens, i32, cfg.B))
 
 
 def pisa_pages_reserve(cfg, pages, add, state, table, lens, grant, moves):
     """Room for add[b] more tokens of each sequence; lens grows by grant[b]."""
     i32, B = torch.int32, cfg.B
-    _paged("pisa_pages_reserve", cfg, pages, (add, i32, B), (state, i32, pisa_pages_state_words(pages)),
+    _paged("pisa_pages_reserve", cfg, pages, (add, i32, B), (state, i32, _state_words(pages)),
            (table, i32, B * pages_width(cfg, pages)), (lens, i32, B), (grant, i32, B), (moves, i32, 4), moves.numel())
 
 
@@ -506,21 +511,21 @@ def pisa_pages_fork(cfg, pages, parent, state, table, lens, table_out, lens_out)
     """Sequence b becomes a copy of sequence parent[b] (outside [0, B): it ends), sharing its pages."""
     i32, B = torch.int32, cfg.B
     n = B * pages_width(cfg, pages)
-    _paged("pisa_pages_fork", cfg, pages, (parent, i32, B), (state, i32, pisa_pages_state_words(pages)), (table, i32, n),
+    _paged("pisa_pages_fork", cfg, pages, (parent, i32, B), (state, i32, _state_words(pages)), (table, i32, n),
            (lens, i32, B), (table_out, i32, n), (lens_out, i32, B))
 
 
 def pisa_pages_free(cfg, pages, seqs, state, table, lens):
     """Ends the listed sequences."""
     i32, B = torch.int32, cfg.B
-    _paged("pisa_pages_free", cfg, pages, (seqs, i32, 0), seqs.numel(), (state, i32, pisa_pages_state_words(pages)),
+    _paged("pisa_pages_free", cfg, pages, (seqs, i32, 0), seqs.numel(), (state, i32, _state_words(pages)),
            (table, i32, B * pages_width(cfg, pages)), (lens, i32, B))
 
 
 def pisa_pages_compact(cfg, pages, state, table, moves):
     """Moves the live pages to the low end of the pool; `moves` lists the copies to make."""
     i32 = torch.int32
-    _paged("pisa_pages_compact", cfg, pages, (state, i32, pisa_pages_state_words(pages)),
+    _paged("pisa_pages_compact", cfg, pages, (state, i32, _state_words(pages)),
            (table, i32, cfg.B * pages_width(cfg, pages)), (moves, i32, 4), moves.numel())
 
 

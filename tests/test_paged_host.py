@@ -77,6 +77,8 @@ def test_sizes(lib):
     assert pisa.pisa_pages_state_words(pisa.make_pages(64, 50)) == 2 * 52 + 3 * 4 + 16
     assert pisa.pisa_pages_state_words(pisa.make_pages(1, 1)) == 2 * 4 + 3 * 4 + 16
     assert lib.pisa_pages_state_words(pisa.make_pages(64, 0)) == -1
+    for P in (1, 4, 5, 31, 32, 33, 127, 129, 100003):   # the binding's own count
+        assert pisa.pisa_pages_state_words(pisa.make_pages(8, P)) == pisa._state_words(pisa.make_pages(8, P))
     pages = pisa.make_pages(64, 50)
     assert pisa.pages_width(_cfg(N=1000), pages) == 16
     one, sixteen = (pisa.pisa_paged_workspace_bytes(_cfg(Hq=2 * g), pages) for g in (1, 16))
