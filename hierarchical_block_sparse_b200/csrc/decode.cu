@@ -498,8 +498,8 @@ __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
         }
         tc::cp_async_wait_all();
         __syncthreads();
-        if (tid < nlist * G) {  // leaf LSE per head (and the PISA-1 / PISA-2 score in s_dot)
-            const int j = tid / G, h = tid - j * G;
+        for (int i = tid; i < nlist * G; i += 256) {  // leaf LSE per head (and the PISA-1 / PISA-2 score in s_dot)
+            const int j = i / G, h = i - j * G;
             float m = -INFINITY, sm = 0.f;
 #pragma unroll
             for (int ww = 0; ww < NW; ++ww) lse_merge(m, sm, s_pm[j][ww][h], s_ps[j][ww][h]);

@@ -425,6 +425,43 @@ def test_sparse_step_equals_the_contiguous_cache(G, d, C, K, S, dtype, N, lens):
         assert torch.equal(x.nan_to_num(5.0), y.nan_to_num(5.0))
 
 
+@pytest.mark.parametrize("paged", [False, True], ids=["contiguous", "paged"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_groups_of_16_rank_every_candidate(d, dtype, paged):
+    # 32 candidate leaves x 16 heads are more than a block has threads: against the oracle's selection
+    from oracle import oracle
+    from tests.parity import TIE_BAND
+    B, Hkv, G, C, K, N, S = 3, 1, 16, 32, 16, 2048, 64
+    cfg = pisa.make_cfg(B=B, Hq=G, Hkv=Hkv, N=N, d=d, C=C, K=K, dtype=dtype)
+    lens = torch.tensor([2000, 1100, 700], dtype=torch.int32)
+    checked = 0
+    for seed in range(3):   # other data each time: what an earlier launch left behind does not fit
+        g = torch.Generator().manual_seed(100 + seed)
+        Kc, Vc = (torch.randn(B, Hkv, N, d, generator=g).to(dtype) for _ in range(2))
+        q = torch.randn(B, G, d, generator=g).to(dtype)
+        new = (lens - 1)[:, None, None, None].long().expand(B, Hkv, 1, d)
+        k, v = (x.gather(2, new)[:, :, 0].contiguous().to(DEV) for x in (Kc, Vc))
+        pyr = torch.zeros(B, Hkv, pisa.pisa_pyramid_rows(cfg), d, device=DEV)
+        pisa.pisa_build_pyramid_prefix(cfg, Kc.to(DEV), (lens - 1).to(DEV), pyr)
+        idx, o = torch.empty(B, Hkv, K, dtype=torch.int32, device=DEV), torch.empty(B, G, d, dtype=dtype, device=DEV)
+        if paged:
+            pool = [x.view(B, Hkv, N // S, S, d).transpose(1, 2).reshape(-1, Hkv, S, d).contiguous().to(DEV) for x in (Kc, Vc)]
+            table = torch.arange(B * N // S, dtype=torch.int32, device=DEV).view(B, -1)
+            pisa.pisa_paged_decode_step(cfg, pisa.make_pages(S, B * N // S), q.to(DEV), k, v, *pool, table, lens.to(DEV), pyr, idx, o)
+        else:
+            pisa.pisa_decode_step(cfg, q.to(DEV), k, v, Kc.to(DEV), Vc.to(DEV), pyr, (lens - 1).to(DEV), idx, o)
+        for b in range(B):
+            n = int(lens[b])
+            Kh = oracle.to_f64(Kc[b, 0, :n])
+            Ph = oracle.build_pyramid(Kh, C, N=n, N_layout=N)
+            want, gap = oracle.select_rows(oracle.to_f64(q[b])[None], np.array([n - 1]), Kh, Ph, C=C, K=K, N=n, N_layout=N)
+            if gap[0] >= TIE_BAND:
+                checked += 1
+                assert idx[b, 0].tolist() == want[0].tolist()
+    assert checked >= 6
+
+
 # ---- as a serving program uses them ------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype,S,C", [(torch.bfloat16, 32, 16), (torch.float32, 16, 16)])
