@@ -202,8 +202,8 @@ int pisa_paged_decode_step(const pisa_cfg* cfg, const pisa_pages* pages, const v
     make_geom(cfg->N, cfg->C, &p.geom);
     p.variant = cfg->score_variant;
     p.table = table; p.S = pages->S; p.P = pages->P; p.W = (int)width(cfg, pages);
-    return cuda_status(launch_decode(cfg->dtype, cfg->d, q_new, K, V, pyr, len, idx, o, k_new, v_new, p,
-                                     (cudaStream_t)stream));
+    return cuda_status(launch_paged_step(cfg->dtype, cfg->d, q_new, k_new, v_new, K, V, len, pyr, idx, o, p,
+                                         (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -15,97 +15,10 @@
 // The same kernel serves the paged cache (PAGED): a page holds whole leaves, so
 // a leaf's rows stay one run of memory and only its first row is looked up,
 // once, when the leaf enters the list; everything downstream is unchanged.
-#include "pisa_internal.h"
-#include "pisa_walk.cuh"
+#include "pisa_decode.cuh"
 #include "tc.cuh"
 
 namespace pisa {
-
-// named barrier over `count` threads (a multiple of 32)
-__device__ __forceinline__ void bar_sync(int id, int count) {
-    asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(count) : "memory");
-}
-
-// Summaries' update of one (b, kv-head) for the row at n: NWA warps (wi =
-// this warp's index among them) write the new key/value row, fetch the leaf's
-// cached rows before n (Kl, Vl: the leaf's first rows; summed per warp,
-// INFLIGHT loads in flight per lane)
-// and the sibling of each ancestor into `scratch` ((NWA + kMaxLevels) x D
-// floats of shared memory) -- none of which depends on the new row -- meet on
-// named barrier `bar`, and warp 0 of them runs the chain leaf -> root.
-template <typename T, int D, int NWA>
-__device__ __forceinline__ void append_unit(T* Kl, T* Vl, float* P, const T* krow, const T* vrow, int64_t n,
-                                            const DecodeParams& p, int wi, int lane, float* scratch, int bar) {
-    constexpr int VD = D / 32;
-    constexpr int INFLIGHT = 8;
-    float* s_part = scratch;            // [NWA][D]
-    float* s_sib = scratch + NWA * D;   // [kMaxLevels][D]
-    float kn[VD];
-    Ld<T, VD>::run(krow + lane * VD, kn);
-    const int64_t leaf = n / p.C, lo = leaf * p.C;
-    if (wi == 0) {
-        float vn[VD];
-        Ld<T, VD>::run(vrow + lane * VD, vn);
-        store_vec<T, VD>(Kl + (n - lo) * D + lane * VD, kn);
-        store_vec<T, VD>(Vl + (n - lo) * D + lane * VD, vn);
-    }
-    float acc[VD];
-#pragma unroll
-    for (int e = 0; e < VD; ++e) acc[e] = 0.f;
-    for (int64_t r0 = lo + wi; r0 < n; r0 += NWA * INFLIGHT) {
-        float x[INFLIGHT][VD];
-#pragma unroll
-        for (int i = 0; i < INFLIGHT; ++i) {
-            const int64_t r = r0 + (int64_t)i * NWA;
-            if (r < n) {
-                Ld<T, VD>::run(Kl + (r - lo) * D + lane * VD, x[i]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VD; ++e) x[i][e] = 0.f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < INFLIGHT; ++i)
-#pragma unroll
-            for (int e = 0; e < VD; ++e) acc[e] += x[i][e];
-    }
-#pragma unroll
-    for (int e = 0; e < VD; ++e) s_part[wi * D + lane * VD + e] = acc[e];
-    const int64_t len = n + 1;
-    for (int l = 1 + wi; l < p.geom.L; l += NWA) {
-        const int64_t sib = (leaf >> (l - 1)) ^ 1;
-        if (sib * ((int64_t)p.C << (l - 1)) < len) {
-            float sv[VD];
-            Ld<float, VD>::run(P + (p.geom.off[l] + sib) * D + lane * VD, sv);
-#pragma unroll
-            for (int e = 0; e < VD; ++e) s_sib[(l - 1) * D + lane * VD + e] = sv[e];
-        }
-    }
-    bar_sync(bar, NWA * 32);
-    if (wi != 0) return;
-    // leaf mean over [leaf*C, n]
-    float m[VD];
-    const float inv = 1.f / (float)(n - lo + 1);
-#pragma unroll
-    for (int e = 0; e < VD; ++e) {
-        float sum = kn[e];
-#pragma unroll
-        for (int w = 0; w < NWA; ++w) sum += s_part[w * D + lane * VD + e];
-        m[e] = sum * inv;
-    }
-    store_vec<float, VD>(P + (p.geom.off[1] + leaf) * D + lane * VD, m);
-    // ancestors: mean of the existing children at length n + 1
-    int64_t node = leaf;
-    for (int l = 1; l < p.geom.L; ++l) {
-        const int64_t sib = node ^ 1;
-        if (sib * ((int64_t)p.C << (l - 1)) < len) {
-#pragma unroll
-            for (int e = 0; e < VD; ++e) m[e] = (m[e] + s_sib[(l - 1) * D + lane * VD + e]) * 0.5f;
-        }
-        node >>= 1;
-        store_vec<float, VD>(P + (p.geom.off[l + 1] + node) * D + lane * VD, m);
-    }
-}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(128) append_kernel(T* __restrict__ Kc, T* __restrict__ Vc,
@@ -147,8 +60,6 @@ struct DecLayout {
     static constexpr int RowsB = 256 / TPR;          // rows per scoring tile
     static constexpr int TPRC = 2 * TPR;             // attention: threads per row
     static constexpr int RowsC = 256 / TPRC;         // rows per attention tile (keys; values alike)
-    static constexpr int TPRW = D / 16;              // walk: threads per fp32 pyramid row
-    static constexpr int RowsW = 256 / TPRW;         // pyramid rows per pass
     static_assert(RowsB * RowBytes == kDecStageBytes, "a scoring tile fills a stage");
     static_assert(2 * RowsC * RowBytes == kDecStageBytes, "an attention tile fills a stage");
     // byte offset of chunk c of row r in a tile whose rows are read by `tpr` threads
@@ -218,15 +129,13 @@ __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
     using Lo = DecLayout<T, D>;
     constexpr int NW = 8;
     constexpr int kDecStages = decode_stages<G>();
-    constexpr int EPC = Lo::EPC, TPR = Lo::TPR, TPRC = Lo::TPRC, TPRW = Lo::TPRW;
+    constexpr int EPC = Lo::EPC, TPR = Lo::TPR, TPRC = Lo::TPRC;
     extern __shared__ __align__(16) uint8_t dsm[];  // pipeline stages, then [NW][G][D] partial outputs
     __shared__ __align__(16) float s_q[G][D];       // scaled queries of the group
-    __shared__ int s_cand[32];
-    __shared__ float s_dot[64][G];
+    __shared__ WalkShared<G> s_walk;
     __shared__ float s_lse[32][G];                  // per candidate slot and head (log2)
     __shared__ int s_sel[32], s_slot[32];
-    __shared__ unsigned s_need;
-    __shared__ int s_level, s_nlist;
+    __shared__ int s_nlist;
     __shared__ float s_Z[G];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -282,98 +191,8 @@ __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
                                   v_new + unit * D, t, p, warp - 1, lane, reinterpret_cast<float*>(dsm), 1);
     }
 
-    // ---- internal levels. Warp 0 carries the walk (lane c = candidate c,
-    // valid candidates in ascending node order) and passes alone through the
-    // levels that need no dot products; at a scored level all threads compute
-    // the <= 64 child dots into s_dot.
-    int cand = lane == 0 ? 0 : -1;  // warp 0's walk state
-    int l = p.geom.L;
-    for (;;) {
-        if (warp == 0) {
-            unsigned need = 0;
-            for (; l >= 2; --l) {
-                const LevelState s = level_state(cand, l, p.C, n_keys, t, 1, F);
-                if (s.n <= p.K) {
-                    const int parent = compact_by_rank(cand, s.vmask, lane >> 1);
-                    cand = lane < 2 * s.n ? 2 * parent + (lane & 1) : -1;
-                    continue;
-                }
-                const unsigned fmask = __ballot_sync(kFull, s.forced);
-                if (__popc(fmask) >= p.K) {  // the forced nodes fill the budget
-                    int id = cand;
-                    const int kept = keep_topk_lane(id, s.forced ? INFINITY : -INFINITY, s.valid, p.K, lane);
-                    const int parent = __shfl_sync(kFull, id, lane >> 1);
-                    cand = lane < 2 * kept ? 2 * parent + (lane & 1) : -1;
-                    continue;
-                }
-                need = s.vmask & ~fmask;
-                break;
-            }
-            s_cand[lane] = cand;
-            if (lane == 0) {
-                s_level = l;
-                s_need = need;
-            }
-        }
-        __syncthreads();
-        const int lv = s_level;
-        if (lv < 2) break;
-        {
-            const unsigned need = s_need;
-            const int64_t span_child = (int64_t)p.C << (lv - 2);
-            const float* child_lvl = P + p.geom.off[lv - 1] * D;
-            const int sl = tid % TPRW;
-#pragma unroll
-            for (int r0 = 0; r0 < 64; r0 += Lo::RowsW) {
-                const int rho = r0 + tid / TPRW, c = rho >> 1;
-                const int64_t child = 2 * (int64_t)s_cand[c] + (rho & 1);
-                const bool ok = ((need >> c) & 1u) && child * span_child < n_keys;
-                float acc[G];
-#pragma unroll
-                for (int h = 0; h < G; ++h) acc[h] = 0.f;
-                if (ok) {
-                    const float4* row = reinterpret_cast<const float4*>(child_lvl + child * D);
-                    float4 x[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x[k] = __ldg(row + sl + TPRW * k);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int e0 = (sl + TPRW * k) * 4;
-#pragma unroll
-                        for (int h = 0; h < G; ++h) {
-                            const float4 qv = *reinterpret_cast<const float4*>(&s_q[h][e0]);
-                            acc[h] = fmaf(qv.x, x[k].x, fmaf(qv.y, x[k].y, fmaf(qv.z, x[k].z, fmaf(qv.w, x[k].w, acc[h]))));
-                        }
-                    }
-                }
-#pragma unroll
-                for (int o = 1; o < TPRW; o <<= 1)
-#pragma unroll
-                    for (int h = 0; h < G; ++h) acc[h] += __shfl_xor_sync(kFull, acc[h], o);
-                if (sl == 0)
-#pragma unroll
-                    for (int h = 0; h < G; ++h) s_dot[rho][h] = acc[h];
-            }
-        }
-        __syncthreads();
-        if (warp == 0) {  // scores (Eq.7, summed over the group: Eq.11) and the keep
-            const LevelState s = level_state(cand, l, p.C, n_keys, t, 1, F);
-            const bool mine = (s_need >> lane) & 1u;
-            float score = -INFINITY;
-            if (mine) {
-                const bool has1 = (2 * (int64_t)cand + 1) * ((int64_t)p.C << (l - 2)) < n_keys;
-                score = 0.f;
-#pragma unroll
-                for (int h = 0; h < G; ++h)
-                    score += pair_score(s_dot[2 * lane][h], has1 ? s_dot[2 * lane + 1][h] : -INFINITY, p.variant);
-            }
-            int id = cand;
-            const int kept = keep_topk_lane(id, s.forced ? INFINITY : score, s.valid, p.K, lane);
-            const int parent = __shfl_sync(kFull, id, lane >> 1);
-            cand = lane < 2 * kept ? 2 * parent + (lane & 1) : -1;
-            --l;
-        }
-    }
+    int cand = 0;  // warp 0's walk state
+    walk_levels<D, G, 256>(P, s_q, s_walk, n_keys, t, F, p, tid, cand);
 
     // ---- leaves: exact LSE (per head) over the raw keys of every valid
     // candidate -- the non-forced ones are ranked by it, and the kept ones
@@ -498,7 +317,7 @@ __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
         }
         tc::cp_async_wait_all();
         __syncthreads();
-        for (int i = tid; i < nlist * G; i += 256) {  // leaf LSE per head (and the PISA-1 / PISA-2 score in s_dot)
+        for (int i = tid; i < nlist * G; i += 256) {  // leaf LSE per head (and the PISA-1 / PISA-2 score in s_walk.dot)
             const int j = i / G, h = i - j * G;
             float m = -INFINITY, sm = 0.f;
 #pragma unroll
@@ -508,48 +327,16 @@ __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
                 Moments mo;
 #pragma unroll
                 for (int ww = 0; ww < NW; ++ww) mo.merge(s_vn[j][ww][h], s_vmean[j][ww][h], s_vm2[j][ww][h]);
-                s_dot[s_slot[j]][h] = mo.score(p.variant);
+                s_walk.dot[s_slot[j]][h] = mo.score(p.variant);
             }
         }
     }
     __syncthreads();
 
-    if (warp == 0) {  // final Top-K (kept leaves come out in ascending order), then Z per head
-        const LevelState s = level_state(cand, 1, p.C, n_keys, t, 1, F);
-        float score = 0.f;  // ranking: the LSE or the PISA-1 / PISA-2 score, summed over the group (Eq.11)
-#pragma unroll
-        for (int h = 0; h < G; ++h) score += s.valid ? (p.variant ? s_dot[lane][h] : s_lse[lane][h]) : 0.f;
-        int id = cand, kept;
-        unsigned kmask;
-        if (s.n <= p.K) {
-            kmask = s.vmask;
-            id = compact_by_rank(cand, s.vmask, lane);
-            kept = s.n;
-        } else {
-            kept = keep_topk_lane(id, s.forced ? INFINITY : score, s.valid, p.K, lane);
-            // kept-ness per candidate lane: the kept ids are in lanes 0..kept-1
-            bool mine = false;
-            for (int i = 0; i < kept; ++i) mine |= (__shfl_sync(kFull, id, i) == cand) && s.valid;
-            kmask = __ballot_sync(kFull, mine);
-        }
-        const int out_id = lane < kept ? id : -1;
-        if (lane < p.K) idx[unit * p.K + lane] = out_id;
-        if ((kmask >> lane) & 1u)  // kept candidate lane -> (its rank among the kept, among the scored)
-            s_kj[__popc(kmask & ((1u << lane) - 1u))] = __popc(s.vmask & ((1u << lane) - 1u));
-        s_sel[lane] = lane < p.K ? out_id : -1;
+    if (warp == 0) {
+        const int out_id = keep_leaves<G>(cand, n_keys, t, F, p, lane, p.variant ? s_walk.dot : s_lse, s_lse, idx + unit * p.K,
+                                          s_sel, s_kj, s_nlist, s_Z);
         if constexpr (PAGED) s_row[lane] = lane < p.K && out_id >= 0 ? leaf_row(out_id) : -1;
-        if (lane == 0) s_nlist = min(kept, p.K);
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-            const float x = ((kmask >> lane) & 1u) ? s_lse[lane][h] : -INFINITY;
-            float m = x;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-            float e = x == -INFINITY ? 0.f : exp2f(x - m);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) e += __shfl_xor_sync(kFull, e, o);
-            if (lane == 0) s_Z[h] = m + log2f(e);
-        }
     }
     __syncthreads();
 

@@ -25,7 +25,7 @@
 
 #include "pisa_internal.h"
 #include "pisa_paged.cuh"
-#include "tc.cuh"
+#include "pisa_tiles.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -35,53 +35,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kStages = 3;
-constexpr int kStageBytes = 8192;  // KT key rows, then KT value rows
+constexpr int kStageBytes = 2 * kTileBytes;  // KT key rows, then KT value rows
 constexpr int kUnitCost = 1;  // 0: 104 us, 1: 77.6, 2: 78.9, 4: 83.1 for 64 sequences of 0..15 K tokens, 32 / 8 heads
 constexpr int kClusterTiles = 4;   // tiles a CTA of a cluster may have to take
-constexpr float kRescale = 8.f;    // see softmax below
-constexpr float kTiny = 1.17549435e-38f;  // smallest normal number
-
-__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool live) {
-    const int bytes = live ? 16 : 0;  // 0: the 16 bytes become zeros, nothing is read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(a)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(a)
-                 : "memory");
-}
-// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), bf16
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// an 8 x 8 matrix of 16-bit elements, two neighbours of a row a lane, transposed
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// Byte offset of 16-byte chunk c of row r of a stage's keys (or values): runs of 128 bytes
-// of all rows one after another, chunks XOR-swizzled by the row so that the 8 rows of
-// one ldmatrix phase hit distinct banks (TMA's 128-byte swizzle; stages are 1 KB aligned).
-template <int Rows>
-__device__ __forceinline__ uint32_t ring_off(int r, int c) {
-    return (uint32_t)((c >> 3) * Rows * 128 + r * 128 + (((c ^ r) & 7) << 4));
-}
 
 // rows [y, y + box) x 128 bytes from x (elements) of a pool into shared memory
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
@@ -95,379 +51,6 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(tc::smem_u32(bar)), "r"(bytes)
                  : "memory");
 }
-
-// ---- one warp's tile, bf16: tensor cores -------------------------------------------
-//
-// S^T = K Q^T and O^T += V^T P^T as m16n8k16 products: the keys (then the dims) are the
-// 16 rows and the group's heads the 8 columns, so a group of up to 8 heads takes half
-// of the products that heads as rows would (G <= 4: 16 instead of 32 a 16 keys). Decode
-// needs 4 G products a key element against 4 bytes of it, far below what even these
-// instructions do per byte of HBM traffic; what they cost is power, and the
-// kernel runs at the power limit.
-// P enters as bf16 high and low parts (2^-16 relative): in one rounding its error would
-// be as large as the output's own. The high part is cut, not rounded, and the low part
-// is kept above zero, so that an infinite value times both stays that infinity. With
-// G <= 4 the columns 4..7 repeat the heads 0..3 and carry the low parts, which then
-// cost nothing; larger groups take a second product.
-template <int D_, int G_>
-struct MmaTile {
-    using T = __nv_bfloat16;
-    static constexpr int D = D_, G = G_;
-    static constexpr int KT = kStageBytes / (2 * D * 2);  // 16 (d = 128) or 32 (d = 64) keys
-    static constexpr int RowBytes = D * 2;
-    static constexpr int kScratchFloats = 0;
-    static constexpr int NT = G > 8 ? 2 : 1;    // column tiles
-    static constexpr bool kTwin = G <= 4;       // columns 4..7 repeat the heads for the low parts
-
-    uint32_t qb[D / 16][NT][2];
-    float o[D / 16][NT][4];  // dims 16 j + g (+ 8), columns 2 c, 2 c + 1 (g = lane / 4, c = lane % 4)
-    float m[NT][2], l[NT][2];  // of this lane's columns; l is this lane's share
-
-    static constexpr bool kAhead = NT == 1;  // registers for the next unit's queries
-    uint32_t qn[kAhead ? D / 16 : 1][NT][2];
-
-    static __device__ __forceinline__ void read_q(uint32_t (*to)[NT][2], const T* q, int lane) {
-        const int g = lane >> 2, c = lane & 3;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int h = kTwin ? g & 3 : 8 * t + g, e = k * 16 + 2 * c + 8 * i;
-                    to[k][t][i] = h < G ? __ldg(reinterpret_cast<const unsigned*>(q + (size_t)h * D + e)) : 0u;
-                }
-    }
-    __device__ __forceinline__ void load_q(const T* q, float, int lane) { read_q(qb, q, lane); }
-    // the next unit's queries: fetched early, taken when their unit begins
-    __device__ __forceinline__ void fetch_q(const T* q, int lane) {
-        if constexpr (kAhead) read_q(qn, q, lane);
-    }
-    __device__ __forceinline__ void take_q(const T* q, float, int lane) {
-        if constexpr (kAhead) {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) qb[k][0][i] = qn[k][0][i];
-        } else {
-            read_q(qb, q, lane);
-        }
-    }
-    __device__ __forceinline__ void reset() {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[j][t][i] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                m[t][i] = -INFINITY;
-                l[t][i] = 0.f;
-            }
-        }
-    }
-    // keys of this tile whose bit is set in `mask` count
-    __device__ __forceinline__ void step(uint32_t kbuf, uint32_t vbuf, unsigned mask, float qscale, int lane, float*) {
-        const int g = lane >> 2, c = lane & 3;
-        float s[KT / 16][NT][4];
-#pragma unroll
-        for (int r = 0; r < KT / 16; ++r) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[r][t][i] = 0.f;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                uint32_t a[4];
-                ldsm4(kbuf + ring_off<KT>(16 * r + (lane & 15), 2 * k + (lane >> 4)), a);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) mma16816(s[r][t], a, qb[k][t][0], qb[k][t][1]);
-            }
-        }
-        // Running maximum: it is only moved when a logit passes it by more than
-        // kRescale (the terms then stay below 2^8, far from overflow), so most tiles
-        // need neither the exchange between lanes nor the rescaling of o.
-        float mx[NT][2];
-        bool move = false;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            mx[t][0] = mx[t][1] = -INFINITY;
-#pragma unroll
-            for (int r = 0; r < KT / 16; ++r)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool live = (mask >> (16 * r + g + 8 * (i >> 1))) & 1u;
-                    s[r][t][i] = live ? s[r][t][i] * qscale : -INFINITY;
-                    mx[t][i & 1] = fmaxf(mx[t][i & 1], s[r][t][i]);
-                }
-            move |= mx[t][0] > m[t][0] + kRescale || mx[t][1] > m[t][1] + kRescale;
-        }
-        if (__any_sync(kFull, move)) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float x = mx[t][i];
-                    x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
-                    x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
-                    x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-                    const float mn = fmaxf(m[t][i], x);
-                    const float a = mn == -INFINITY ? 1.f : exp2f(m[t][i] - mn);
-                    m[t][i] = mn;
-                    l[t][i] *= a;
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        o[j][t][i] *= a;
-                        o[j][t][i + 2] *= a;
-                    }
-                }
-        }
-#pragma unroll
-        for (int r = 0; r < KT / 16; ++r) {
-            uint32_t hi[NT][2], lo[NT][2];  // P^T: keys 0..7 and 8..15 of the 16
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float p0 = ex2_approx(s[r][t][2 * i] - m0), p1 = ex2_approx(s[r][t][2 * i + 1] - m1);
-                    l[t][0] += p0;
-                    l[t][1] += p1;
-                    const unsigned u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
-                    const uint32_t h = __byte_perm(u0, u1, 0x7632);
-                    const uint32_t w = pack_bf16(fmaxf(p0 - __uint_as_float(u0 & 0xffff0000u), kTiny),
-                                                 fmaxf(p1 - __uint_as_float(u1 & 0xffff0000u), kTiny));
-                    if constexpr (kTwin) {
-                        hi[t][i] = transpose8(c < 2 ? h : w);
-                    } else {
-                        hi[t][i] = transpose8(h);
-                        lo[t][i] = transpose8(w);
-                    }
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-                uint32_t a[4];
-                ldsm4_t(vbuf + ring_off<KT>(16 * r + (lane >> 4) * 8 + (lane & 7), 2 * j + ((lane >> 3) & 1)), a);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    mma16816(o[j][t], a, hi[t][0], hi[t][1]);
-                    if constexpr (!kTwin) mma16816(o[j][t], a, lo[t][0], lo[t][1]);
-                }
-            }
-        }
-    }
-    __device__ __forceinline__ void poison() {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) l[t][0] = l[t][1] = NAN;
-    }
-    // this warp's state into a merge slot ([G][D] o, then m[G], l[G]); `add`: merged with what is there
-    __device__ __forceinline__ void put(float* slot, bool add, int lane) {
-        const int g = lane >> 2, c = lane & 3;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int h = 8 * t + 2 * c + i;
-                const bool mine = h < G && (!kTwin || c < 2);
-                float sum = l[t][i];
-                sum += __shfl_xor_sync(kFull, sum, 4);
-                sum += __shfl_xor_sync(kFull, sum, 8);
-                sum += __shfl_xor_sync(kFull, sum, 16);
-                float a = 1.f, b = 0.f, mn = m[t][i];
-                if (add && mine) {
-                    const float ms = slot[G * D + h];
-                    mn = fmaxf(mn, ms);
-                    a = m[t][i] == -INFINITY ? 0.f : exp2f(m[t][i] - mn);
-                    b = ms == -INFINITY ? 0.f : exp2f(ms - mn);
-                    sum = a * sum + b * slot[G * D + G + h];
-                }
-                __syncwarp();
-                if (mine && g == 0) {
-                    slot[G * D + h] = mn;
-                    slot[G * D + G + h] = sum;
-                }
-#pragma unroll
-                for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float x = o[j][t][i + 2 * e];
-                        if (kTwin) x += __shfl_xor_sync(kFull, x, 2);  // the low parts' column
-                        float* p = slot + h * D + 16 * j + 8 * e + g;
-                        if (mine) *p = add ? a * x + b * *p : x;
-                    }
-            }
-    }
-};
-
-// ---- one warp's tile, fp32: CUDA cores -----------------------------------------------
-//
-// A lane owns 4 dims of a row (D / 4 lanes a row, 32 * 4 / D rows at a time);
-// the G partial dots of several rows are summed across lanes in one
-// reduce-scatter, and the probabilities come back through shared memory.
-template <int D_, int G_>
-struct FmaTile {
-    using T = float;
-    static constexpr int D = D_, G = G_;
-    static constexpr int KT = kStageBytes / (2 * D * 4);  // 8 (d = 128) or 16 (d = 64) keys
-    static constexpr int RowBytes = D * 4;
-    static constexpr int LR = D / 4;       // lanes a row
-    static constexpr int RP = 32 / LR;     // rows at a time
-    static constexpr int RI = KT / RP;     // rows a lane takes part in
-    static constexpr int kScratchFloats = KT * G + G;
-    static constexpr int NB = RI * G < LR ? RI * G : LR;  // values of one reduce-scatter
-
-    float q[G][4], o[G][4];
-    float m, l;  // of head lane % G (G <= 16 lanes hold it several times over; l is a share)
-
-    __device__ __forceinline__ void fetch_q(const T*, int) {}
-    __device__ __forceinline__ void take_q(const T* src, float qscale, int lane) { load_q(src, qscale, lane); }
-    __device__ __forceinline__ void load_q(const T* src, float qscale, int lane) {
-        const int e = (lane % LR) * 4;
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(src + (size_t)h * D + e));
-            q[h][0] = v.x * qscale;
-            q[h][1] = v.y * qscale;
-            q[h][2] = v.z * qscale;
-            q[h][3] = v.w * qscale;
-        }
-    }
-    __device__ __forceinline__ void reset() {
-#pragma unroll
-        for (int h = 0; h < G; ++h)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[h][e] = 0.f;
-        m = -INFINITY;
-        l = 0.f;
-    }
-    static __device__ __forceinline__ float4 row16(uint32_t buf, int r, int c) {
-        float4 v;
-        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];\n"
-                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                     : "r"(buf + ring_off<KT>(r, c))
-                     : "memory");
-        return v;
-    }
-    __device__ __forceinline__ void step(uint32_t kbuf, uint32_t vbuf, unsigned mask, float, int lane, float* scratch) {
-        const int sub = lane / LR, c = lane % LR;
-        constexpr int RowsB = NB / G;  // rows (of this lane's) in one reduce-scatter
-#pragma unroll
-        for (int r0 = 0; r0 < RI; r0 += RowsB) {
-            float v[NB];
-#pragma unroll
-            for (int r = 0; r < RowsB; ++r) {
-                const float4 x = row16(kbuf, (r0 + r) * RP + sub, c);
-#pragma unroll
-                for (int h = 0; h < G; ++h)
-                    v[r * G + h] = fmaf(q[h][0], x.x, fmaf(q[h][1], x.y, fmaf(q[h][2], x.z, q[h][3] * x.w)));
-            }
-            int n = NB;
-#pragma unroll
-            for (int w = LR / 2; w >= 1; w >>= 1) {
-                if (n > 1) {
-                    n >>= 1;
-                    const bool hi = (lane & w) != 0;
-#pragma unroll
-                    for (int i = 0; i < NB / 2; ++i)
-                        if (i < n) {
-                            const float send = hi ? v[i] : v[i + n], keep = hi ? v[i + n] : v[i];
-                            v[i] = keep + __shfl_xor_sync(kFull, send, w);
-                        }
-                } else {
-                    v[0] += __shfl_xor_sync(kFull, v[0], w);
-                }
-            }
-            const int i = (lane % LR) / (LR / NB);  // the value this lane ended with
-            scratch[((r0 + i / G) * RP + sub) * G + i % G] = v[0];
-        }
-        __syncwarp();
-        // head h = lane % G, keys lane / G, lane / G + 32 / G, ...
-        constexpr int PER = (KT * G + 31) / 32;
-        const int h = lane % G;
-        float z[PER], mx = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int key = lane / G + i * (32 / G);
-            z[i] = key < KT && ((mask >> key) & 1u) ? scratch[key * G + h] : -INFINITY;
-            mx = fmaxf(mx, z[i]);
-        }
-#pragma unroll
-        for (int w = G; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, w));
-        const bool move = __any_sync(kFull, mx > m + kRescale);
-        if (move) {
-            const float mn = fmaxf(m, mx);
-            const float a = mn == -INFINITY ? 1.f : exp2f(m - mn);
-            m = mn;
-            l *= a;
-            if (lane < G) scratch[KT * G + lane] = a;
-        }
-        const float mu = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int key = lane / G + i * (32 / G);
-            if (key < KT) {
-                const float p = exp2f(z[i] - mu);
-                l += p;
-                scratch[key * G + h] = p;
-            }
-        }
-        __syncwarp();
-        if (move) {
-#pragma unroll
-            for (int hh = 0; hh < G; ++hh) {
-                const float a = scratch[KT * G + hh];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[hh][e] *= a;
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < RI; ++r) {
-            const int key = r * RP + sub;
-            const float4 x = row16(vbuf, key, c);
-#pragma unroll
-            for (int hh = 0; hh < G; ++hh) {
-                const float p = scratch[key * G + hh];
-                o[hh][0] = fmaf(p, x.x, o[hh][0]);
-                o[hh][1] = fmaf(p, x.y, o[hh][1]);
-                o[hh][2] = fmaf(p, x.z, o[hh][2]);
-                o[hh][3] = fmaf(p, x.w, o[hh][3]);
-            }
-        }
-        __syncwarp();  // scratch is rewritten by the next tile
-    }
-    __device__ __forceinline__ void poison() { l = NAN; }
-    __device__ __forceinline__ void put(float* slot, bool add, int lane) {
-        float sum = l;
-#pragma unroll
-        for (int w = G; w < 32; w <<= 1) sum += __shfl_xor_sync(kFull, sum, w);
-        float a = 1.f, b = 0.f, mn = m;
-        if (add) {
-            const float ms = slot[G * D + lane % G];
-            mn = fmaxf(m, ms);
-            a = m == -INFINITY ? 0.f : exp2f(m - mn);
-            b = ms == -INFINITY ? 0.f : exp2f(ms - mn);
-            sum = a * sum + b * slot[G * D + G + lane % G];
-        }
-        __syncwarp();
-        if (lane < G) {
-            slot[G * D + lane] = mn;
-            slot[G * D + G + lane] = sum;
-        }
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-            const float ah = __shfl_sync(kFull, a, h), bh = __shfl_sync(kFull, b, h);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float x = o[h][e];
-                if (RP == 2) x += __shfl_xor_sync(kFull, x, LR);  // the two rows' shares of a dim
-                float* p = slot + h * D + (lane % LR) * 4 + e;
-                if (lane < LR) *p = add ? ah * x + bh * *p : x;
-            }
-        }
-    }
-};
 
 // ---- the list of tiles ------------------------------------------------------------------
 
@@ -916,17 +499,6 @@ __global__ void __launch_bounds__(128) paged_join_kernel(T* __restrict__ out, fl
 using PFN_encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// shared memory above 48 KB: asked for once a device and kernel
-template <class Kern>
-cudaError_t allow_smem(Kern kern, int bytes, std::atomic<uint64_t>& done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) >> dev) & 1)) return e;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
-    return e;
-}
 
 // TMA's view of a pool: all rows of all pages, in boxes of `rows` x 128 bytes
 bool row_map(CUtensorMap* map, const void* pool, const PagedParams& p, int rows, int d, int elem) {

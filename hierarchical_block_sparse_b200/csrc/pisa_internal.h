@@ -134,6 +134,9 @@ int check_gpu_cfg(const pisa_cfg* c);
 struct PagedParams;
 cudaError_t launch_paged_attn(int dtype, int d, const void* q, const void* k_new, const void* v_new, void* K, void* V,
                               void* o, float* lse, void* ws, const PagedParams& p, int sms, cudaStream_t st);
+cudaError_t launch_paged_step(int dtype, int d, const void* q, const void* k_new, const void* v_new, void* K, void* V,
+                              const int32_t* len, float* pyr, int32_t* idx, void* o, const DecodeParams& p,
+                              cudaStream_t st);
 cudaError_t launch_paged_append(int row_bytes, const void* k_new, const void* v_new, int T, const int32_t* count, void* K,
                                 void* V, const PagedParams& p, cudaStream_t st);
 cudaError_t launch_pages_init(int32_t* state, int32_t* table, int32_t* len, int B, int P, int W, cudaStream_t st);

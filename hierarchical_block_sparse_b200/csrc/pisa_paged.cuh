@@ -24,6 +24,17 @@ inline int sm_count() {
     return sms;
 }
 
+// shared memory above 48 KB: asked for once a device and kernel
+template <class Kern>
+inline cudaError_t allow_smem(Kern kern, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) >> dev) & 1)) return e;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+    return e;
+}
+
 // The attention's workspace holds two parts for each of at most this many CTAs.
 constexpr int kPagedMaxCtas = 512;
 

@@ -381,17 +381,38 @@ def test_append_rows(T, S, d, Hkv, dtype):
 
 # ---- the sparse step over pages --------------------------------------------------------------
 
-@pytest.mark.parametrize("G,d,C,K,S,dtype,N,lens", [
+def _selected64(q, K, V, idx, n, C, G):
+    """Attention of one token over its leaves idx [Hkv, K] of K, V [Hkv, N, d], and what its tolerance needs; in 64 bits."""
+    Hq, d = q.shape
+    o, size = torch.zeros(Hq, d, dtype=torch.float64), torch.zeros(Hq, 2, dtype=torch.float64)
+    for h in range(Hq):
+        pos = torch.cat([torch.arange(int(i) * C, min(int(i) * C + C, n)) for i in idx[h // G] if i >= 0])
+        k, v, x = K[h // G, pos].double(), V[h // G, pos].double(), q[h].double()
+        o[h] = torch.softmax((k @ x) / math.sqrt(d), 0) @ v
+        size[h, 0], size[h, 1] = ((k.abs() @ x.abs()) / math.sqrt(d)).max(), v.abs().max()
+    return o, size
+
+
+STEPS = [
     (1, 128, 64, 8, 64, torch.bfloat16, 4096, [1000, 2049, 3001, 1]),
     (2, 128, 64, 8, 128, torch.bfloat16, 4000, [1000, 2048, 3999, 64]),
     (1, 64, 16, 4, 48, torch.float32, 1024, [100, 512, 990, 17]),
     (4, 64, 32, 8, 32, torch.bfloat16, 2048, [333, 1024, 2000, 31]),
+    (8, 128, 64, 16, 64, torch.bfloat16, 4096, [4000, 1600, 63, 1023]),
+    (8, 128, 64, 16, 64, torch.float32, 4096, [4000, 1600, 63, 1023]),
+    (16, 64, 24, 16, 24, torch.float32, 2048, [2040, 700, 23, 500]),
+    (2, 64, 7, 5, 14, torch.bfloat16, 500, [490, 7, 8, 300]),        # leaves that end inside a tile
+    (16, 128, 64, 16, 64, torch.bfloat16, 4096, [4000, 1600, 63, 1023]),
     (16, 128, 128, 4, 256, torch.bfloat16, 4096, [1500, 2600, 4050, 128]),
-])
-def test_sparse_step_equals_the_contiguous_cache(G, d, C, K, S, dtype, N, lens):
+    (4, 128, 1024, 16, 1024, torch.float32, 20000, [19000, 16500, 5, 1025]),   # logits too many to keep
+]
+
+
+@pytest.mark.parametrize("G,d,C,K,S,dtype,N,lens,variant", [x + (0,) for x in STEPS] + [x + (v,) for x in STEPS[:4] for v in (1, 2)])
+def test_sparse_step_chooses_and_attends_as_the_contiguous_cache(G, d, C, K, S, dtype, N, lens, variant):
     B, Hkv = len(lens), 2
     g = torch.Generator().manual_seed(13)
-    cfg = pisa.make_cfg(B=B, Hq=Hkv * G, Hkv=Hkv, N=N, d=d, C=C, K=K, dtype=dtype)
+    cfg = pisa.make_cfg(B=B, Hq=Hkv * G, Hkv=Hkv, N=N, d=d, C=C, K=K, dtype=dtype, score_variant=variant)
     W = -(-N // S)
     P = B * W + 3
     table = torch.randperm(P, generator=g)[:B * W].view(B, W).int().to(DEV)
@@ -405,6 +426,7 @@ def test_sparse_step_equals_the_contiguous_cache(G, d, C, K, S, dtype, N, lens):
     pisa.pisa_build_pyramid_prefix(cfg, Kc, n, pyr)
     pisa.pisa_paged_build_pyramid(cfg, pages, Kp, table, n, pyp)
     assert torch.equal(pyr, pyp)
+    other = 0
     for _ in range(4):
         q = torch.randn(B, Hkv * G, d, generator=g).to(dtype).to(DEV)
         k, v = (torch.randn(B, Hkv, d, generator=g).to(dtype).to(DEV) for _ in range(2))
@@ -414,7 +436,18 @@ def test_sparse_step_equals_the_contiguous_cache(G, d, C, K, S, dtype, N, lens):
         n = n + 1
         pisa.pisa_paged_decode_step(cfg, pages, q, k, v, Kp, Vp, table, n, pyp, idp, op)
         torch.cuda.synchronize()
-        assert torch.equal(idx, idp) and torch.equal(o, op) and torch.equal(pyr, pyp)
+        # a summary is a mean of C rows in 32 bits, in an order of the kernel's
+        assert float((pyr - pyp).abs().max()) <= 2 * C * 2.0 ** -24 * float(Kc.abs().max())
+        other += int((idx != idp).any(-1).sum())   # a tie to 32 bits may fall either way
+        host = [x.cpu() for x in (q, Kc, Vc, idp, op)]
+        for b in range(B):
+            if int(n[b]) > N:
+                assert bool((idp[b] == -1).all()) and not op[b].any()
+                continue
+            ro, size = _selected64(host[0][b], host[1][b], host[2][b], host[3][b], int(n[b]), C, G)
+            tol, _ = tolerances(ro[None], torch.zeros(1, G * Hkv), size[None], [K * C], d, dtype)
+            assert bool(((host[4][b].double() - ro).abs() <= tol[0]).all())
+    assert other <= 1
     # out of range, no page for the token: untouched, idx -1, o 0
     bad = torch.tensor([0, N + 1, -3, lens[3]], dtype=torch.int32, device=DEV)
     table[3, (lens[3] - 1) // S] = P
@@ -460,6 +493,33 @@ def test_groups_of_16_rank_every_candidate(d, dtype, paged):
                 checked += 1
                 assert idx[b, 0].tolist() == want[0].tolist()
     assert checked >= 6
+
+
+def test_sparse_step_without_some_leaves():
+    # leaves whose page is missing count as empty: never read, and nothing of them in the output
+    B, Hkv, G, d, C, K, S, N = 1, 2, 2, 128, 64, 16, 64, 2048
+    g = torch.Generator().manual_seed(21)
+    cfg = pisa.make_cfg(B=B, Hq=Hkv * G, Hkv=Hkv, N=N, d=d, C=C, K=K)
+    P = 40
+    table = torch.randperm(P, generator=g)[:32].view(1, 32).int()
+    Kp, Vp = (torch.randn(P, Hkv, S, d, generator=g).bfloat16() for _ in range(2))
+    n, gone = 1000, [3, 7, 14]
+    dev = [x.to(DEV) for x in (Kp, Vp, table)]
+    pyr = torch.zeros(B, Hkv, pisa.pisa_pyramid_rows(cfg), d, device=DEV)
+    pages, lens = pisa.make_pages(S, P), torch.tensor([n], dtype=torch.int32, device=DEV)
+    pisa.pisa_paged_build_pyramid(cfg, pages, dev[0], dev[2], lens, pyr)
+    dev[2][0, gone] = torch.tensor([-1, P, 10 ** 9], dtype=torch.int32, device=DEV)
+    q, k, v = (torch.randn(B, h, d, generator=g).bfloat16() for h in (Hkv * G, Hkv, Hkv))
+    idx, o = torch.empty(B, Hkv, K, dtype=torch.int32, device=DEV), torch.empty(B, Hkv * G, d, dtype=torch.bfloat16, device=DEV)
+    pisa.pisa_paged_decode_step(cfg, pages, q.to(DEV), k.to(DEV), v.to(DEV), *dev, lens, pyr, idx, o)
+    rows = [x[table[0].long()].transpose(0, 1).reshape(Hkv, N, d).clone() for x in (Kp, Vp)]
+    for x, y in zip(rows, (k, v)):
+        x[:, n - 1] = y[0]
+    here = [i for i in range(16) if i not in gone]
+    want = torch.tensor(here).expand(Hkv, -1)
+    ro, size = _selected64(q[0], rows[0], rows[1], want, n, C, G)
+    tol, _ = tolerances(ro[None], torch.zeros(1, G * Hkv), size[None], [K * C], d, torch.bfloat16)
+    assert bool(((o[0].cpu().double() - ro).abs() <= tol[0]).all())
 
 
 # ---- as a serving program uses them ------------------------------------------------------------
