@@ -1,18 +1,20 @@
 // paged_step.cu -- the sparse decode step (close reading §5.1, §5.3) over a paged cache.
 //
-// One CTA of 4 warps per (sequence, KV head), in four phases:
+// One CTA of 4 or 8 warps per (sequence, KV head), in four phases:
 //   1. append and the walk of the internal levels, as in decode.cu (shared code);
 //   2. the keys of every candidate leaf stream past the group's queries; the logits stay
-//      in shared memory (32 leaves x C keys x G heads). Each warp takes every 4th tile
-//      of KT keys through a ring of its own, with no barrier in between;
+//      in shared memory (32 leaves x C keys x G heads). The warps take tiles of KT keys in
+//      turn, each through a ring of its own, with no barrier in between;
 //   3. log-sum-exps from those logits, and the final choice;
 //   4. the values of the kept leaves alone stream past 2^(z - Z).
 // decode.cu sums a key's products on the CUDA cores with the queries read from
 // shared memory, G times for every element, and merges softmax states a tile at a
 // time: from G = 4 on that is what its time goes to. Here phases 2 and 4 cost 16
 // tensor-core products a 16 keys (fp32: the queries stay in registers) and the
-// softmax is taken once. What bounds this kernel is the chain of dependent phases at
-// 4 CTAs an SM: while all of them walk, HBM is idle.
+// softmax is taken once: 64 sequences of 12 to 16 K tokens, 8 heads: 139.8 -> 82.7 us (84%
+// of the HBM floor of 69.5); 8 heads a group at 665 tokens: 174 -> 35 us (fp32: 225 -> 62);
+// 16 a group at 8 K: 432 -> 62 us. What bounds it is the chain of dependent phases: about
+// 13 us of walk, one level after another, in which HBM is idle.
 #include "pisa_decode.cuh"
 #include "pisa_paged.cuh"
 #include "pisa_tiles.cuh"
@@ -21,13 +23,10 @@ namespace pisa {
 
 namespace {
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kStages = 2;
-
 // floats a head's logits of one leaf take: whole tiles, and 4 so that heads fall into different banks
 __host__ __device__ constexpr int logit_stride(int C, int kt) { return (C + kt - 1) / kt * kt + 4; }
 
-template <class Tile>
+template <class Tile, int kWarps, int kStages>
 size_t step_smem(int C, int K) {
     const size_t ring = (size_t)kWarps * kStages * kTileBytes;
     const size_t slots = sizeof(float) * kWarps * Tile::G * (Tile::D + 1);
@@ -37,14 +36,14 @@ size_t step_smem(int C, int K) {
     return (head + 15) / 16 * 16 + sizeof(float) * ((size_t)2 * K * Tile::G * logit_stride(C, Tile::KT) + kWarps * Tile::kScratchFloats);
 }
 
-template <class Tile>
-__global__ void __launch_bounds__(kThreads, Tile::G <= 4 ? 4 : Tile::G <= 8 ? 3 : 2) paged_step_kernel(
+template <class Tile, int kWarps, int kStages>
+__global__ void __launch_bounds__(kWarps * 32, kWarps > 4 ? 1 : Tile::G <= 4 ? 4 : Tile::G <= 8 ? 3 : 2) paged_step_kernel(
     const typename Tile::T* __restrict__ q_new, const typename Tile::T* __restrict__ k_new,
     const typename Tile::T* __restrict__ v_new, typename Tile::T* __restrict__ K, typename Tile::T* __restrict__ V,
     const int32_t* __restrict__ len, float* __restrict__ pyr, int32_t* __restrict__ idx, typename Tile::T* __restrict__ out,
     int z_at, DecodeParams p) {
     using T = typename Tile::T;
-    constexpr int D = Tile::D, G = Tile::G, KT = Tile::KT;
+    constexpr int D = Tile::D, G = Tile::G, KT = Tile::KT, kThreads = kWarps * 32;
     constexpr int CPR = Tile::RowBytes / 16, RPI = 32 / CPR;
     extern __shared__ __align__(128) uint8_t dyn[];  // rings (append: scratch; at the end: slots), logits, scratch
     __shared__ __align__(16) float s_q[G][D];
@@ -77,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, Tile::G <= 4 ? 4 : Tile::G <= 8 ? 3 
     const Forced F(t, p.C, 1, p.forced_mask);
     for (int i = tid; i < G * D; i += kThreads) s_q[i / D][i % D] = (float)q_new[head0 * D + i] * p.qscale;
     __syncthreads();
-    // the append runs on warps 1..3 while warp 0 passes the first levels, which never read what it rewrites
+    // the append runs on the other warps while warp 0 passes the first levels, which never read what it rewrites
     if (warp >= 1)
         append_unit<T, D, kWarps - 1>(K + (size_t)new_row * D, V + (size_t)new_row * D, P, k_new + (size_t)unit * D,
                                       v_new + (size_t)unit * D, t, p, warp - 1, lane, reinterpret_cast<float*>(dyn), 1);
@@ -102,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, Tile::G <= 4 ? 4 : Tile::G <= 8 ? 3 
     const int nlist = s_nlist;
     const uint32_t ring = tc::smem_u32(dyn) + warp * kStages * kTileBytes;
     auto rows_of = [&](int j) { return s_row[j] < 0 ? 0 : min(p.C, n_keys - s_sel[j] * p.C); };  // keys of scored leaf j
-    // streams tiles warp, warp + 4, ... of `tiles` through the ring; at(i, j, r0): tile i is rows r0.. of scored leaf j
+    // streams every kWarps-th of `tiles` through this warp's ring; at(i, j, r0): tile i is rows r0.. of scored leaf j
     auto stream = [&](const T* pool, int tiles, auto at, auto use) {
         auto issue = [&](int i, int stage) {
             if (i < tiles) {
@@ -186,23 +185,37 @@ __global__ void __launch_bounds__(kThreads, Tile::G <= 4 ? 4 : Tile::G <= 8 ? 3 
     }
 }
 
-template <class Tile>
-cudaError_t launch_step(const void* q, const void* k_new, const void* v_new, void* K, void* V, const int32_t* len,
-                        float* pyr, int32_t* idx, void* o, const DecodeParams& p, cudaStream_t st, bool* taken) {
+template <class Tile, int kWarps, int kStages>
+cudaError_t launch_shape(const void* q, const void* k_new, const void* v_new, void* K, void* V, const int32_t* len,
+                         float* pyr, int32_t* idx, void* o, const DecodeParams& p, cudaStream_t st, bool* taken) {
     using T = typename Tile::T;
-    const size_t smem = step_smem<Tile>(p.C, p.K);
+    const size_t smem = step_smem<Tile, kWarps, kStages>(p.C, p.K);
     // static: queries, dots, log-sum-exps; all of an SM's 227 KB at most
     const size_t fixed = sizeof(float) * (Tile::G * Tile::D + 97 * Tile::G) + 2048;
     *taken = smem + fixed <= (size_t)227 * 1024;
     if (!*taken) return cudaSuccess;
-    auto kern = paged_step_kernel<Tile>;
+    auto kern = paged_step_kernel<Tile, kWarps, kStages>;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(kern, 227 * 1024 - (int)fixed, done);
     if (e != cudaSuccess) return e;
     const int z_at = (int)(smem - sizeof(float) * ((size_t)2 * p.K * Tile::G * logit_stride(p.C, Tile::KT) + kWarps * Tile::kScratchFloats));
-    kern<<<(unsigned)(p.B * p.Hkv), kThreads, smem, st>>>((const T*)q, (const T*)k_new, (const T*)v_new, (T*)K, (T*)V, len, pyr,
-                                                          idx, (T*)o, z_at, p);
+    kern<<<(unsigned)(p.B * p.Hkv), kWarps * 32, smem, st>>>((const T*)q, (const T*)k_new, (const T*)v_new, (T*)K, (T*)V, len,
+                                                             pyr, idx, (T*)o, z_at, p);
     return cudaGetLastError();
+}
+
+// Up to one unit an SM: 8 warps and a longer ring each, for a CTA has its SM alone (64 units
+// of 4 x 8 heads at 32 K tokens: 63 us with 4 warps, 42 with 8). More units: 4 warps, so that 4
+// (G <= 4) share an SM (256 units of 8 heads at 665 tokens: 35 us, 44 with 8 warps).
+template <class Tile>
+cudaError_t launch_step(const void* q, const void* k_new, const void* v_new, void* K, void* V, const int32_t* len,
+                        float* pyr, int32_t* idx, void* o, const DecodeParams& p, cudaStream_t st, bool* taken) {
+    if ((int64_t)p.B * p.Hkv <= sm_count()) {
+        cudaError_t e = launch_shape<Tile, 8, 3>(q, k_new, v_new, K, V, len, pyr, idx, o, p, st, taken);
+        if (!*taken && e == cudaSuccess) e = launch_shape<Tile, 8, 2>(q, k_new, v_new, K, V, len, pyr, idx, o, p, st, taken);
+        if (*taken || e != cudaSuccess) return e;
+    }
+    return launch_shape<Tile, 4, 2>(q, k_new, v_new, K, V, len, pyr, idx, o, p, st, taken);
 }
 
 template <int D, int G>
