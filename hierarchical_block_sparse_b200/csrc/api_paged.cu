@@ -144,8 +144,8 @@ int pisa_paged_append(const pisa_cfg* cfg, const pisa_pages* pages, const void* 
 int64_t pisa_paged_workspace_bytes(const pisa_cfg* cfg, const pisa_pages* pages) {
     const int s = check(cfg, pages);
     if (s) return s;
-    // two parts a CTA: o, then maximum and sum, for each head of a group
-    return (int64_t)kPagedMaxCtas * 2 * (cfg->Hq / cfg->Hkv) * (cfg->d + 2) * (int64_t)sizeof(float);
+    // two parts a CTA: o, then maximum and sum, for each head of a group; and what there is to join
+    return (int64_t)kPagedMaxCtas * (2 * (cfg->Hq / cfg->Hkv) * (cfg->d + 2) + 2) * (int64_t)sizeof(float);
 }
 
 int pisa_paged_attn(const pisa_cfg* cfg, const pisa_pages* pages, const void* q, const void* k_new, const void* v_new,
@@ -154,6 +154,7 @@ int pisa_paged_attn(const pisa_cfg* cfg, const pisa_pages* pages, const void* q,
     const int s = check(cfg, pages);
     if (s) return s;
     if (cfg->causal != 1) return PISA_E_INVALID;  // the new token sees only the past
+    if ((int64_t)cfg->B * cfg->Hkv * (cfg->N / 32 + 2) >= ((int64_t)1 << 31)) return PISA_E_UNSUPPORTED;  // 32-bit list of tiles
     if (cfg->N == 0) return PISA_OK;
     if (!q || !K || !V || K == V || !table || !len || !o || !workspace) return PISA_E_INVALID;
     if ((k_new == nullptr) != (v_new == nullptr)) return PISA_E_INVALID;

@@ -470,7 +470,7 @@ def _refuse(name, t, dtype, n, dev):
 def _paged(name: str, cfg, pages, *args) -> None:
     """Call `name` with tensors given as (tensor, dtype, least number of elements) and
     plain numbers as they are, on the tensors' device and its current stream."""
-    dev, out = -1, []
+    dev, out = -2, []
     for a in args:
         if type(a) is tuple:
             t, dtype, n = a

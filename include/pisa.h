@@ -471,7 +471,8 @@ int64_t pisa_paged_workspace_bytes(const pisa_cfg *cfg, const pisa_pages *pages)
  * sequence without keys gives o = 0, lse = -inf. With k_new, v_new ([B, Hkv, d];
  * both or neither) the token len[b] - 1 is written into its page on the way, as
  * pisa_paged_append with T = 1 would. C, K, g, forced_mask and score_variant
- * do not matter. Equal inputs give equal bits. A wait for a copy that takes over
+ * do not matter. B*Hkv*(N/32 + 2) >= 2^31 gives PISA_E_UNSUPPORTED. Equal inputs give
+ * equal bits. A wait for a copy that takes over
  * about a second is given up; the sequences it concerns get NaN. workspace: 16-byte aligned,
  * contents arbitrary, nothing is kept in it; calls that share one must not
  * overlap on the GPU. */
