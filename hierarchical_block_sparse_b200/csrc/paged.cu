@@ -220,8 +220,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
         const int pos = lt * TK + warp * KT + lane;
         page = left > 0 && lane < KT && pos < ln ? __ldg(p.table + (size_t)lb * p.W + pos / p.S) : -1;
     };
-    // the token in hand lies in this warp's rows of tile t of a sequence of n keys
-    auto fresh_at = [&](int t, int n) { return k_new != nullptr && (n - 1) / TK == t && ((n - 1) % TK) / KT == warp; };
+    // the token in hand lies in this warp's rows of tile t of sequence b (n keys; a length past N has none)
+    auto fresh_at = [&](int b, int t, int n) {
+        return k_new != nullptr && (n - 1) / TK == t && ((n - 1) % TK) / KT == warp && p.len[b] == n;
+    };
     auto issue_rows = [&](int stage) {
         const int pos = lt * TK + warp * KT + lane;
         const bool live = lane < KT && pos < ln && page >= 0 && page < p.P;
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
         if (lane == 0) sm.mask[warp][stage] = mask;
         const uint32_t kbuf = tc::smem_u32(sm.ring[warp][stage]), vbuf = kbuf + kStageBytes / 2;
         const int c = lane % CPR;
-        const bool fresh = fresh_at(lt, ln);
+        const bool fresh = fresh_at(lb, lt, ln);
 #pragma unroll
         for (int i = 0; i < KT / RPI; ++i) {
             const int r = i * RPI + lane / CPR;
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
                 }
             }
         }
-        if (live && fresh_at(lt, ln) && lane < CPR) {  // into its page; the ring gets it when the stage is used
+        if (live && fresh_at(lb, lt, ln) && lane < CPR) {  // into its page; the ring gets it when the stage is used
             const size_t u = ((size_t)lb * p.Hkv + lh) * D + lane * (16 / sizeof(T));
             const size_t e = (size_t)(row + (ln - 1) % KT) * D + lane * (16 / sizeof(T));
             *reinterpret_cast<uint4*>(K + e) = __ldg(reinterpret_cast<const uint4*>(k_new + u));
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
                 tile.poison();  // the result is NaN
             } else if (mask != 0) {
                 const int rows = __popc(mask);
-                const bool fresh = fresh_at(t, n);
+                const bool fresh = fresh_at(b, t, n);
                 if (rows < KT || fresh) {
                     // rows past the end may hold anything: their values count as zeros. The token in hand
                     // comes from its rows (its page may have been read before they were there).

@@ -470,7 +470,7 @@ int64_t pisa_paged_workspace_bytes(const pisa_cfg *cfg, const pisa_pages *pages)
  * (written; may be NULL), the natural log of the sum of exponentials. A
  * sequence without keys gives o = 0, lse = -inf. With k_new, v_new ([B, Hkv, d];
  * both or neither) the token len[b] - 1 is written into its page on the way, as
- * pisa_paged_append with T = 1 would. C, K, g, forced_mask and score_variant
+ * pisa_paged_append with T = 1 and count 1 would. C, K, g, forced_mask and score_variant
  * do not matter. B*Hkv*(N/32 + 2) >= 2^31 gives PISA_E_UNSUPPORTED. Equal inputs give
  * equal bits. A wait for a copy that takes over
  * about a second is given up; the sequences it concerns get NaN. workspace: 16-byte aligned,

@@ -143,6 +143,62 @@ def test_attention_with_the_token_appended_on_the_way(d, S, dtype):
     _check(o, lse, q, K1, V1, table, n, S, 4)
 
 
+def test_a_length_past_the_capacity_appends_nothing():
+    for S in (64, 24):   # rows by TMA, by single copies
+        cfg, pages, q, K, V, table, n = _cache([640, 640], Hkv=2, G=2, d=128, S=S, N=640, dtype=torch.bfloat16, seed=16)
+        k_new, v_new = torch.full((2, 2, 128), 9.0).bfloat16(), torch.full((2, 2, 128), 9.0).bfloat16()
+        lens = torch.tensor([641, 640], dtype=torch.int32)
+        o, lse, K1, V1 = _attend(cfg, pages, q, K, V, table, lens, k_new, v_new)
+        page, row = table[:, 639 // S].long(), 639 % S
+        assert torch.equal(K1[page[0], :, row], K[page[0], :, row]) and bool((K1[page[1], :, row] == 9).all())
+        _check(o, lse, q, K1, V1, table, lens.clamp(max=640), S, 2)
+
+
+@pytest.mark.parametrize("S,n,B", [(64, 5000, 3), (64, 200, 1), (24, 5000, 3)], ids=["tma", "cluster", "copies"])
+def test_pools_past_32_bit_offsets(S, n, B):
+    # 10 GB of keys, and as much of values: the pages in use lie at the end
+    Hkv, G, d = 8, 2, 128
+    P = 40_000_000 // (Hkv * S)
+    cfg = pisa.make_cfg(B=B, Hq=Hkv * G, Hkv=Hkv, N=n, d=d, C=8, K=4)
+    pages, W = pisa.make_pages(S, P), -(-n // S)
+    K, V = (torch.empty(P, Hkv, S, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    assert K.numel() > 2 ** 32
+    g = torch.Generator().manual_seed(17)
+    table = (P - 1 - torch.randperm(B * W + 5, generator=g)[:B * W]).view(B, W).int().to(DEV)
+    lens = torch.tensor([n - b for b in range(B)], dtype=torch.int32, device=DEV)
+    k, v = (torch.randn(B, Hkv, n, d, generator=g).bfloat16() for _ in range(2))
+    pisa.pisa_paged_append(cfg, pages, k.to(DEV), v.to(DEV), lens, lens, table, K, V)
+    q = torch.randn(B, Hkv * G, d, generator=g).bfloat16()
+    o, lse = torch.empty(B, Hkv * G, d, dtype=torch.bfloat16, device=DEV), torch.empty(B, Hkv * G, device=DEV)
+    pisa.pisa_paged_attn(cfg, pages, q.to(DEV), None, None, K, V, table, lens, o, lse, pisa.alloc_paged_workspace(cfg, pages, DEV))
+    small = [x.view(B, Hkv, n, 1, d).transpose(1, 2).reshape(B * n, Hkv, 1, d) for x in (k, v)]
+    flat = torch.arange(B * n, dtype=torch.int32).view(B, n)
+    _check(o.cpu(), lse.cpu(), q, *small, flat, lens.cpu(), 1, G)
+    moves = torch.tensor([1, 0, 0, 0, int(table[0, 0]), P - 1 - (B * W + 10)], dtype=torch.int32, device=DEV)
+    pisa.pisa_pages_copy(cfg, pages, moves, K, V)
+    torch.cuda.synchronize()
+    rows = min(S, n)
+    assert torch.equal(K[int(moves[5]), :, :rows].cpu(), k[0, :, :rows]) and torch.equal(V[int(moves[5]), :, :rows].cpu(), v[0, :, :rows])
+
+
+def test_two_calls_at_once():
+    # two streams, a workspace each, one cache
+    cfg, pages, q, K, V, table, lens = [x.to(DEV) if torch.is_tensor(x) else x for x in
+                                        _cache([30000, 77, 5000], Hkv=2, G=4, d=128, S=64, N=30000, dtype=torch.bfloat16, seed=18)]
+    ws = [pisa.alloc_paged_workspace(cfg, pages, DEV) for _ in range(2)]
+    want = torch.empty_like(q)
+    pisa.pisa_paged_attn(cfg, pages, q, None, None, K, V, table, lens, want, None, ws[0])
+    outs = [[torch.empty_like(q) for _ in range(20)] for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i in range(20):
+        for s in range(2):
+            with torch.cuda.stream(streams[s]):
+                pisa.pisa_paged_attn(cfg, pages, q, None, None, K, V, table, lens, outs[s][i], None, ws[s])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for group in outs for o in group)
+
+
 def test_attention_gives_equal_bits_and_leaves_its_inputs():
     case = _cache([5000, 3, 0, 900], Hkv=2, G=8, d=128, S=16, N=5000, dtype=torch.bfloat16, seed=8)
     first = _attend(*case)
