@@ -21,27 +21,39 @@ __device__ __forceinline__ void drop(int32_t* refs, unsigned* bits, int page, in
     else if (old <= 0) atomicAdd(refs + page, 1);  // a table that names a free page: leave the page free
 }
 
-// exclusive sum over the 1024 threads of a block; *total gets the sum of all
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
+// exclusive sums of N values over the 1024 threads of a block; total[i] gets the sums of all
+template <int N>
+__device__ __forceinline__ void block_scan(int64_t (&v)[N], int64_t (&warp_sums)[N][32], int64_t (&total)[N]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t x = v;
+    int64_t x[N], s[N];
 #pragma unroll
-    for (int w = 1; w < 32; w <<= 1) {
-        const int64_t y = __shfl_up_sync(kFull, x, w);
-        if (lane >= w) x += y;
-    }
-    __syncthreads();  // warp_sums may still be read from the scan before
-    if (lane == 31) warp_sums[warp] = x;
+    for (int i = 0; i < N; ++i) x[i] = v[i];
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int64_t y = __shfl_up_sync(kFull, x[i], w);
+            if (lane >= w) x[i] += y;
+        }
+    if (lane == 31)
+#pragma unroll
+        for (int i = 0; i < N; ++i) warp_sums[i][warp] = x[i];
     __syncthreads();
-    int64_t s = warp_sums[lane];
 #pragma unroll
-    for (int w = 1; w < 32; w <<= 1) {
-        const int64_t y = __shfl_up_sync(kFull, s, w);
-        if (lane >= w) s += y;
+    for (int i = 0; i < N; ++i) s[i] = warp_sums[i][lane];
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int64_t y = __shfl_up_sync(kFull, s[i], w);
+            if (lane >= w) s[i] += y;
+        }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        total[i] = __shfl_sync(kFull, s[i], 31);
+        const int64_t before = __shfl_sync(kFull, s[i], (warp + 31) & 31);
+        v[i] = (warp == 0 ? 0 : before) + x[i] - v[i];
     }
-    *total = __shfl_sync(kFull, s, 31);
-    const int64_t before = __shfl_sync(kFull, s, (warp + 31) & 31);
-    return (warp == 0 ? 0 : before) + x - v;
 }
 
 __global__ void __launch_bounds__(256) pages_init_kernel(int32_t* __restrict__ state, int32_t* __restrict__ table,
@@ -69,7 +81,7 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const int32_t* __re
                                                              int32_t* __restrict__ table, int32_t* __restrict__ len,
                                                              int32_t* __restrict__ grant, int32_t* __restrict__ moves,
                                                              int B, int N, int S, int P, int W) {
-    __shared__ int64_t warp_sums[32];
+    __shared__ int64_t warp_sums[2][32];
     __shared__ int s_shared;                         // sequences with a shared partial last page
     __shared__ int s_ids[kReserveIds];               // the first pages handed out
     extern __shared__ int dyn[];                     // two arrays of that list, then four of the sequences
@@ -86,14 +98,16 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const int32_t* __re
     int32_t* ids = state + L.map();
     // free pages, counted in order of their ids, a run of words a thread (the bitmap is
     // padded to 4 words); read first, so that the loads overlap the sequences'
-    const int words = (P + 31) / 32, run = ((words + 1023) / 1024 + 3) / 4 * 4;
+    const int words = (P + 31) / 32, run = words <= 1024 ? 1 : ((words + 1023) / 1024 + 3) / 4 * 4;
     const int w0 = tid * run, w1 = min(w0 + run, words);
-    uint4 head = make_uint4(0u, 0u, 0u, 0u);
-    if (w0 < w1) head = *reinterpret_cast<const uint4*>(bits + w0);
-    int64_t found = __popc(head.x) + __popc(head.y) + __popc(head.z) + __popc(head.w);
-    for (int w = w0 + 4; w < w1; w += 4) {
-        const uint4 v = *reinterpret_cast<const uint4*>(bits + w);
-        found += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
+    int64_t found = 0;
+    if (run == 1) {
+        if (w0 < w1) found = __popc(bits[w0]);
+    } else {
+        for (int w = w0; w < w1; w += 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(bits + w);
+            found += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
+        }
     }
     if (tid == 0) s_shared = 0;
     __syncthreads();
@@ -128,7 +142,7 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const int32_t* __re
         }
     }
     __syncthreads();
-    int64_t mine = 0;  // copies << 48 | pages
+    int64_t sums[2] = {0, found}, all[2];  // copies << 48 | pages of this thread's sequences; its free pages
 #pragma unroll
     for (int i = 0; i < kReservePer; ++i) {
         if (tail[i] >= 0) {
@@ -136,33 +150,39 @@ __global__ void __launch_bounds__(1024) pages_reserve_kernel(const int32_t* __re
             for (int k = 0; k < s_shared; ++k) before += l_page[k] == tail[i] && l_seq[k] < b0 + i;
             if (before >= refs[tail[i]] - 1) tail[i] = -1;  // the last holder writes in place
         }
-        mine += (int64_t)(want[i] - have[i]) + (tail[i] >= 0 ? ((int64_t)1 << 48) + 1 : 0);
+        sums[0] += (int64_t)(want[i] - have[i]) + (tail[i] >= 0 ? ((int64_t)1 << 48) + 1 : 0);
     }
-    int64_t all;
-    int64_t at = block_scan(mine, warp_sums, &all);
-    const int64_t total = all & (((int64_t)1 << 48) - 1);
-
-    int64_t spare;
-    int64_t rank = block_scan(found, warp_sums, &spare);
+    block_scan(sums, warp_sums, all);
+    int64_t at = sums[0], rank = sums[1];
+    const int64_t total = all[0] & (((int64_t)1 << 48) - 1), spare = all[1];
     const bool fits = total <= spare;
     if (tid == 0) {
-        moves[0] = fits ? (int)(all >> 48) : 0;
+        moves[0] = fits ? (int)(all[0] >> 48) : 0;
         moves[1] = fits ? 0 : (int)min(total - spare, (int64_t)INT32_MAX);
         moves[2] = (int)(P - spare + (fits ? total : 0));
         moves[3] = (int)(spare - (fits ? total : 0));
     }
     if (fits) {
-        for (int w = w0; w < w1 && rank < total; ++w) {
-            unsigned v = w == w0 ? head.x : w == w0 + 1 ? head.y : w == w0 + 2 ? head.z : w == w0 + 3 ? head.w : bits[w];
-            const unsigned was = v;
-            while (v && rank < total) {
-                const int page = w * 32 + __ffs(v) - 1;
-                if (rank < kReserveIds) s_ids[rank] = page;
-                else ids[rank] = page;
-                ++rank;
-                v &= v - 1;
+        // the first `total` of them, a word at a time by a whole warp, a bit a lane
+        const int lane = tid & 31;
+        unsigned busy = __ballot_sync(kFull, found > 0 && rank < total);
+        while (busy) {
+            const int from = __ffs(busy) - 1;
+            busy &= busy - 1;
+            int64_t at_rank = __shfl_sync(kFull, rank, from);
+            const int first = __shfl_sync(kFull, w0, from), last = __shfl_sync(kFull, w1, from);
+            for (int w = first; w < last && at_rank < total; ++w) {
+                const unsigned v = bits[w];
+                const int64_t k = at_rank + __popc(v & ((1u << lane) - 1u));
+                const bool mine = (v >> lane) & 1u, taken = mine && k < total;
+                if (taken) {
+                    if (k < kReserveIds) s_ids[k] = w * 32 + lane;
+                    else ids[k] = w * 32 + lane;
+                }
+                const unsigned left = __ballot_sync(kFull, mine && !taken);
+                if (lane == 0 && left != v) bits[w] = left;
+                at_rank += __popc(v);
             }
-            if (v != was) bits[w] = v;
         }
     }
 #pragma unroll
@@ -241,7 +261,7 @@ __global__ void __launch_bounds__(256) pages_free_kernel(const int32_t* __restri
 // Compaction, 1 of 3: live pages before each word of the bitmap, the bitmap as it
 // was and as it will be (pages below the live count taken, the others free).
 __global__ void __launch_bounds__(1024) compact_scan_kernel(int32_t* __restrict__ state, int32_t* __restrict__ moves, int P) {
-    __shared__ int64_t warp_sums[32];
+    __shared__ int64_t warp_sums[1][32];
     const PageState L(P);
     unsigned* bits = reinterpret_cast<unsigned*>(state + L.bits());
     unsigned* old = reinterpret_cast<unsigned*>(state + L.old_bits());
@@ -253,10 +273,11 @@ __global__ void __launch_bounds__(1024) compact_scan_kernel(int32_t* __restrict_
         const int left = P - w * 32;
         return left >= 32 ? v : v & ((1u << left) - 1u);
     };
-    int64_t mine = 0;
-    for (int w = w0; w < w1; ++w) mine += __popc(taken(w));
-    int64_t live;
-    int64_t at = block_scan(mine, warp_sums, &live);
+    int64_t sums[1] = {0}, all[1];
+    for (int w = w0; w < w1; ++w) sums[0] += __popc(taken(w));
+    block_scan(sums, warp_sums, all);
+    const int64_t live = all[0];
+    int64_t at = sums[0];
     for (int w = w0; w < w1; ++w) {
         const unsigned v = taken(w);
         before[w] = (int)at;
