@@ -130,11 +130,11 @@ template <class Tile>
 struct Smem {
     static constexpr int kSlotFloats = Tile::G * (Tile::D + 2);
     // merge slots: one a warp where they fit beside the ring twice an SM, else warps take turns
-    static constexpr int kRoom = 115712 - kWarps * kStages * kStageBytes - kWarps * (Tile::kScratchFloats + 1) * 4 - 256;
+    static constexpr int kRoom = 115712 - kWarps * kStages * kStageBytes - kWarps * (Tile::kScratchFloats + 4) * 4 - 256;
     static constexpr int kSlots = 4 * kSlotFloats * 4 <= kRoom ? 4 : 2 * kSlotFloats * 4 <= kRoom ? 2 : 1;
     alignas(1024) uint8_t ring[kWarps][kStages][kStageBytes];
     float slot[kSlots][kSlotFloats];
-    float scratch[kWarps][Tile::kScratchFloats + 1];
+    alignas(16) float scratch[kWarps][Tile::kScratchFloats + 4];
     unsigned mask[kWarps][kStages];
     uint64_t full[kWarps][kStages];  // TMA: a stage's rows have landed
     // a cluster's CTA: its part of the unit ([G][D] o, then m[G], l[G]), over the ring

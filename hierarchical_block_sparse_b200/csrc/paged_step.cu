@@ -33,7 +33,7 @@ size_t step_smem(int C, int K) {
     const size_t scratch = (size_t)(kWarps - 1 + kMaxLevels) * Tile::D * sizeof(float);  // the append's
     size_t head = ring > slots ? ring : slots;
     if (scratch > head) head = scratch;
-    return (head + 15) / 16 * 16 + sizeof(float) * ((size_t)2 * K * Tile::G * logit_stride(C, Tile::KT) + kWarps * Tile::kScratchFloats);
+    return (head + 15) / 16 * 16 + sizeof(float) * ((size_t)2 * K * Tile::G * logit_stride(C, Tile::KT) + kWarps * Tile::kWeighFloats);
 }
 
 template <class Tile, int kWarps, int kStages>
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps > 4 ? 1 : Tile::G <= 4 ? 4
     const int unit = blockIdx.x, b = unit / p.Hkv, kvh = unit % p.Hkv;
     float* z = reinterpret_cast<float*>(dyn + z_at);
     const int zs = logit_stride(p.C, KT);
-    float* scratch = z + 2 * p.K * G * zs + warp * Tile::kScratchFloats;
+    float* scratch = z + 2 * p.K * G * zs + warp * Tile::kWeighFloats;
     const int t = len[b] - 1;
     auto leaf_row = [&](int leaf) -> int {  // its first row of the pool (pages hold whole leaves); -1: no page
         const int tok = leaf * p.C;
@@ -198,7 +198,7 @@ cudaError_t launch_shape(const void* q, const void* k_new, const void* v_new, vo
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(kern, 227 * 1024 - (int)fixed, done);
     if (e != cudaSuccess) return e;
-    const int z_at = (int)(smem - sizeof(float) * ((size_t)2 * p.K * Tile::G * logit_stride(p.C, Tile::KT) + kWarps * Tile::kScratchFloats));
+    const int z_at = (int)(smem - sizeof(float) * ((size_t)2 * p.K * Tile::G * logit_stride(p.C, Tile::KT) + kWarps * Tile::kWeighFloats));
     kern<<<(unsigned)(p.B * p.Hkv), kWarps * 32, smem, st>>>((const T*)q, (const T*)k_new, (const T*)v_new, (T*)K, (T*)V, len,
                                                              pyr, idx, (T*)o, z_at, p);
     return cudaGetLastError();

@@ -73,7 +73,7 @@ struct MmaTile {
     static constexpr int D = D_, G = G_;
     static constexpr int KT = kTileBytes / (D * 2);  // 16 (d = 128) or 32 (d = 64) keys
     static constexpr int RowBytes = D * 2;
-    static constexpr int kScratchFloats = 0;
+    static constexpr int kScratchFloats = 0, kWeighFloats = 0;
     static constexpr int NT = G > 8 ? 2 : 1;    // column tiles
     static constexpr bool kTwin = G <= 4;       // columns 4..7 repeat the heads for the low parts
 
@@ -351,7 +351,32 @@ struct MmaTile {
 //
 // A lane owns 4 dims of a row (D / 4 lanes a row, 32 * 4 / D rows at a time);
 // the G partial dots of several rows are summed across lanes in one
-// reduce-scatter, and the probabilities come back through shared memory.
+// reduce-scatter, and the probabilities come back through shared memory (each twice,
+// as the operand of a packed product). Products are packed pairs (fma.rn.f32x2): with
+// groups of 8 and 16 the kernel is bound by instructions, not by memory.
+
+struct Pair {  // two floats in a 64-bit register
+    uint64_t v;
+};
+__device__ __forceinline__ Pair pair_of(float a, float b) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b));
+    return p;
+}
+__device__ __forceinline__ void unpair(const Pair& p, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
+}
+__device__ __forceinline__ Pair fma2(const Pair& a, const Pair& b, const Pair& c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+__device__ __forceinline__ Pair mul2(const Pair& a, const Pair& b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+
 template <int D_, int G_>
 struct FmaTile {
     using T = float;
@@ -361,10 +386,12 @@ struct FmaTile {
     static constexpr int LR = D / 4;       // lanes a row
     static constexpr int RP = 32 / LR;     // rows at a time
     static constexpr int RI = KT / RP;     // rows a lane takes part in
-    static constexpr int kScratchFloats = KT * G + G;
+    static constexpr int kScratchFloats = (3 * KT * G + G + 3) / 4 * 4;  // p twice, logits, factors
+    static constexpr int kZ = 2 * KT * G, kA = 3 * KT * G;
+    static constexpr int kWeighFloats = 2 * KT * G;  // of which weigh() needs these
     static constexpr int NB = RI * G < LR ? RI * G : LR;  // values of one reduce-scatter
 
-    float q[G][4], o[G][4];
+    Pair q[G][2], o[G][2];
     float m, l;  // of head lane % G (G <= 16 lanes hold it several times over; l is a share)
 
     __device__ __forceinline__ void fetch_q(const T*, int) {}
@@ -374,27 +401,20 @@ struct FmaTile {
 #pragma unroll
         for (int h = 0; h < G; ++h) {
             const float4 v = __ldg(reinterpret_cast<const float4*>(src + (size_t)h * D + e));
-            q[h][0] = v.x * qscale;
-            q[h][1] = v.y * qscale;
-            q[h][2] = v.z * qscale;
-            q[h][3] = v.w * qscale;
+            q[h][0] = pair_of(v.x * qscale, v.y * qscale);
+            q[h][1] = pair_of(v.z * qscale, v.w * qscale);
         }
     }
     __device__ __forceinline__ void reset() {
 #pragma unroll
         for (int h = 0; h < G; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[h][e] = 0.f;
+            for (int e = 0; e < 2; ++e) o[h][e] = pair_of(0.f, 0.f);
         m = -INFINITY;
         l = 0.f;
     }
-    static __device__ __forceinline__ float4 row16(uint32_t buf, int r, int c) {
-        float4 v;
-        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];\n"
-                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                     : "r"(buf + ring_off<KT>(r, c))
-                     : "memory");
-        return v;
+    static __device__ __forceinline__ void row16(uint32_t buf, int r, int c, Pair (&x)[2]) {
+        asm volatile("ld.shared.v2.b64 {%0,%1}, [%2];\n" : "=l"(x[0].v), "=l"(x[1].v) : "r"(buf + ring_off<KT>(r, c)) : "memory");
     }
     // z[h * hs + key * ks] = logits of the tile's keys
     __device__ __forceinline__ void dots(uint32_t kbuf, float* z, int hs, int ks, int lane) {
@@ -405,10 +425,14 @@ struct FmaTile {
             float v[NB];
 #pragma unroll
             for (int r = 0; r < RowsB; ++r) {
-                const float4 x = row16(kbuf, (r0 + r) * RP + sub, c);
+                Pair x[2];
+                row16(kbuf, (r0 + r) * RP + sub, c, x);
 #pragma unroll
-                for (int h = 0; h < G; ++h)
-                    v[r * G + h] = fmaf(q[h][0], x.x, fmaf(q[h][1], x.y, fmaf(q[h][2], x.z, q[h][3] * x.w)));
+                for (int h = 0; h < G; ++h) {
+                    float a, b;
+                    unpair(fma2(q[h][0], x[0], mul2(q[h][1], x[1])), a, b);
+                    v[r * G + h] = a + b;
+                }
             }
             int n = NB;
 #pragma unroll
@@ -430,25 +454,33 @@ struct FmaTile {
             z[(i % G) * hs + ((r0 + i / G) * RP + sub) * ks] = v[0];
         }
     }
-    // o += p v, p[key * G + h]
+    // o += p v, p[2 * (key * G + h)] and the float behind it
     __device__ __forceinline__ void accumulate(uint32_t vbuf, const float* p, int lane) {
         const int sub = lane / LR, c = lane % LR;
 #pragma unroll
         for (int r = 0; r < RI; ++r) {
             const int key = r * RP + sub;
-            const float4 x = row16(vbuf, key, c);
+            Pair x[2], w[G];
+            row16(vbuf, key, c, x);
+            const uint32_t at = tc::smem_u32(p + 2 * key * G);
+            if constexpr (G == 1) {
+                asm volatile("ld.shared.b64 %0, [%1];\n" : "=l"(w[0].v) : "r"(at) : "memory");
+            } else {
 #pragma unroll
-            for (int h = 0; h < G; ++h) {
-                const float w = p[key * G + h];
-                o[h][0] = fmaf(w, x.x, o[h][0]);
-                o[h][1] = fmaf(w, x.y, o[h][1]);
-                o[h][2] = fmaf(w, x.z, o[h][2]);
-                o[h][3] = fmaf(w, x.w, o[h][3]);
+                for (int h = 0; h < G; h += 2)
+                    asm volatile("ld.shared.v2.b64 {%0,%1}, [%2];\n" : "=l"(w[h].v), "=l"(w[h + 1].v) : "r"(at + 8 * h) : "memory");
             }
+#pragma unroll
+            for (int h = 0; h < G; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) o[h][e] = fma2(w[h], x[e], o[h][e]);
         }
     }
+    static __device__ __forceinline__ void put_p(float* scratch, int key, int h, float p) {
+        *reinterpret_cast<float2*>(scratch + 2 * (key * G + h)) = make_float2(p, p);
+    }
     __device__ __forceinline__ void step(uint32_t kbuf, uint32_t vbuf, unsigned mask, float, int lane, float* scratch) {
-        dots(kbuf, scratch, 1, G, lane);
+        dots(kbuf, scratch + kZ, 1, G, lane);
         __syncwarp();
         // head h = lane % G, keys lane / G, lane / G + 32 / G, ...
         constexpr int PER = (KT * G + 31) / 32;
@@ -457,7 +489,7 @@ struct FmaTile {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int key = lane / G + i * (32 / G);
-            z[i] = key < KT && ((mask >> key) & 1u) ? scratch[key * G + h] : -INFINITY;
+            z[i] = key < KT && ((mask >> key) & 1u) ? scratch[kZ + key * G + h] : -INFINITY;
             mx = fmaxf(mx, z[i]);
         }
 #pragma unroll
@@ -468,7 +500,7 @@ struct FmaTile {
             const float a = mn == -INFINITY ? 1.f : exp2f(m - mn);
             m = mn;
             l *= a;
-            if (lane < G) scratch[KT * G + lane] = a;
+            if (lane < G) scratch[kA + lane] = a;
         }
         const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll
@@ -477,20 +509,25 @@ struct FmaTile {
             if (key < KT) {
                 const float p = exp2f(z[i] - mu);
                 l += p;
-                scratch[key * G + h] = p;
+                put_p(scratch, key, h, p);
             }
         }
         __syncwarp();
         if (move) {
 #pragma unroll
             for (int hh = 0; hh < G; ++hh) {
-                const float a = scratch[KT * G + hh];
+                const Pair a = pair_of(scratch[kA + hh], scratch[kA + hh]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[hh][e] *= a;
+                for (int e = 0; e < 2; ++e) o[hh][e] = mul2(o[hh][e], a);
             }
         }
         accumulate(vbuf, scratch, lane);
         __syncwarp();  // scratch is rewritten by the next tile
+    }
+    __device__ __forceinline__ float part_of(int h, int e) const {
+        float a, b;
+        unpair(o[h][e >> 1], a, b);
+        return e & 1 ? b : a;
     }
     __device__ __forceinline__ void poison() { l = NAN; }
 
@@ -507,7 +544,7 @@ struct FmaTile {
             if (key < KT) {
                 const float p = key < rows ? exp2f(z[h * stride + key] - Z[h]) : 0.f;
                 l += p;
-                scratch[key * G + h] = p;
+                put_p(scratch, key, h, p);
             }
         }
         __syncwarp();
@@ -523,7 +560,7 @@ struct FmaTile {
         for (int h = 0; h < G; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float x = o[h][e];
+                float x = part_of(h, e);
                 if (RP == 2) x += __shfl_xor_sync(kFull, x, LR);
                 if (lane < LR) slot[h * D + lane * 4 + e] = x;
             }
@@ -550,7 +587,7 @@ struct FmaTile {
             const float ah = __shfl_sync(kFull, a, h), bh = __shfl_sync(kFull, b, h);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float x = o[h][e];
+                float x = part_of(h, e);
                 if (RP == 2) x += __shfl_xor_sync(kFull, x, LR);  // the two rows' shares of a dim
                 float* p = slot + h * D + (lane % LR) * 4 + e;
                 if (lane < LR) *p = add ? ah * x + bh * *p : x;
