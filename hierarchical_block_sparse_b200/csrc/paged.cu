@@ -3,14 +3,14 @@
 //   z_j = q . k_j / sqrt(d) over the len[b] cached keys;  o = sum_j e^(z_j) v_j / sum_j e^(z_j)
 //
 // One pass over the keys and values with a running maximum and sum (in log2
-// units). The work is a list of tiles of TK keys, ordered by (sequence, KV
-// head, position); CTA c of `grid` takes the c-th equal share of that list,
-// whatever the lengths, so one long sequence and many short ones load the
-// GPU alike. Beginning and ending a (sequence, KV head) unit costs about as
-// much as a tile, which the list counts in front of the unit's own (kUnitCost). A (sequence, KV head) unit that falls into one share is finished
-// by its CTA; one that is cut leaves (max, sum, unnormalised o) of each part in
-// the workspace, which paged_join_kernel joins in share order (the result
-// depends on the lengths alone, not on timing).
+// units). The work is a list of tiles of TK keys, ordered by (sequence, KV head,
+// position); CTA c takes the c-th equal share of that list, whatever the lengths, so
+// one long sequence and many short ones load the GPU alike. Beginning and ending a
+// (sequence, KV head) unit costs about as much as a tile, which the list counts in
+// front of the unit's own (kUnitCost). A unit that falls into one share is finished by
+// its CTA; one that is cut leaves (max, sum, unnormalised o) of each part in the
+// workspace, which paged_join_kernel joins in share order (the result depends on the
+// lengths alone, not on timing).
 //
 // Few and short units (see launch_tile) go without list and join: a cluster of up
 // to 8 CTAs takes one unit and joins its parts through its shared memory.
@@ -20,6 +20,13 @@
 // warp that waits for memory holds up no other. The rows come by TMA where a page
 // holds whole groups of KT rows, else by cp.async, which takes any page size (and
 // starts sooner: the clusters use it).
+//
+// Bound by HBM: every byte is read once (16 sequences of 16 K tokens, 8 KV heads: 1.071 GB
+// of DRAM reads for 1.068 GB of keys and values; tensor pipe 10%, issue slots 27% busy).
+// 64 such sequences take 640 us, 256 K tokens of one 159 us (101% and 103% of a copy's
+// bandwidth, back to back). Both run at the board's power limit, so what took
+// instructions away made them faster: heads as the 8 columns of a product instead of its
+// 16 rows 729 -> 696 us, TMA instead of cp.async 696 -> 640.
 #include <cooperative_groups.h>
 #include <cuda.h>  // CUtensorMap
 
@@ -37,7 +44,8 @@ constexpr int kWarps = 4;
 constexpr int kStages = 3;
 constexpr int kStageBytes = 2 * kTileBytes;  // KT key rows, then KT value rows
 constexpr int kUnitCost = 1;  // 0: 104 us, 1: 77.6, 2: 78.9, 4: 83.1 for 64 sequences of 0..15 K tokens, 32 / 8 heads
-constexpr int kClusterTiles = 4;   // tiles a CTA of a cluster may have to take
+constexpr int kClusterTiles = 4;  // most tiles for a cluster's CTA (1 K tokens, 8 heads: 6.3 us, by the list 7.2 and a second
+                                  // launch; 4 K tokens, 32 units in fp32: 11.9, by the list 9.2)
 
 // rows [y, y + box) x 128 bytes from x (elements) of a pool into shared memory
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {

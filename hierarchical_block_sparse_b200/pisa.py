@@ -453,96 +453,103 @@ def _elem(cfg):
     return torch.bfloat16 if cfg.dtype == PISA_DTYPE_BF16 else torch.float32
 
 
-def _pool(cfg, pages):
-    return pages.P * cfg.Hkv * pages.S * cfg.d
+def _state_words(pages):
+    P = pages.P
+    return 2 * (P + 3 & ~3) + 3 * ((P + 31) // 32 + 3 & ~3) + 16
 
 
-def _refuse(name, t, dtype, n, dev):
-    if not t.is_cuda:
+# These calls are made at every token: one check and one pointer a tensor, no lists.
+
+def _dev(t) -> int:
+    d = t.get_device()
+    if d < 0:
         raise ValueError("tensors must live on a CUDA device")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: tensors on different devices ({dev}, {t.get_device()})")
-    if not t.is_contiguous():
-        raise ValueError("tensors must be contiguous")
-    raise ValueError(f"{name}: expected at least {n} elements of {dtype}, got {t.numel()} of {t.dtype}")
+    return d
 
 
-def _paged(name: str, cfg, pages, *args) -> None:
-    """Call `name` with tensors given as (tensor, dtype, least number of elements) and
-    plain numbers as they are, on the tensors' device and its current stream."""
-    dev, out = -2, []
-    for a in args:
-        if type(a) is tuple:
-            t, dtype, n = a
-            if t is None:
-                a = None
-            else:
-                d = t.get_device()
-                if d != dev and (dev >= 0 or d < 0) or t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
-                    _refuse(name, t, dtype, n, dev if dev >= 0 else d)
-                dev = d
-                a = t.data_ptr()
-        out.append(a)
-    fn = getattr(_lib or load(), name)
+def _at(t, dtype, n, dev):
+    """The address of t, which holds at least n elements of dtype on device dev."""
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous() or t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError("tensors must live on a CUDA device")
+        if t.get_device() != dev:
+            raise ValueError(f"tensors on different devices ({dev}, {t.get_device()})")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        raise ValueError(f"expected at least {n} elements of {dtype}, got {t.numel()} of {t.dtype}")
+    return t.data_ptr()
+
+
+def _go(dev, fn, *args) -> None:
+    """fn on device dev and its current stream."""
     if dev == torch._C._cuda_getDevice():
-        status = fn(cfg, pages, *out, torch._C._cuda_getCurrentRawStream(dev))
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(cfg, pages, *out, torch._C._cuda_getCurrentRawStream(dev))
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if status != 0:
-        _check(name, status)
+        _check(fn.__name__, status)
+
+
+_i32 = torch.int32
 
 
 def pisa_pages_init(cfg, pages, state, table, lens):
     """An empty cache: every page free, table -1, lengths 0."""
-    i32 = torch.int32
-    _paged("pisa_pages_init", cfg, pages, (state, i32, _state_words(pages)),
-           (table, i32, cfg.B * pages_width(cfg, pages)), (lens, i32, cfg.B))
+    dev, B = _dev(state), cfg.B
+    _go(dev, (_lib or load()).pisa_pages_init, cfg, pages, _at(state, _i32, _state_words(pages), dev),
+        _at(table, _i32, B * -(-cfg.N // pages.S), dev), _at(lens, _i32, B, dev))
 
 
 def pisa_pages_reserve(cfg, pages, add, state, table, lens, grant, moves):
     """Room for add[b] more tokens of each sequence; lens grows by grant[b]."""
-    i32, B = torch.int32, cfg.B
-    _paged("pisa_pages_reserve", cfg, pages, (add, i32, B), (state, i32, _state_words(pages)),
-           (table, i32, B * pages_width(cfg, pages)), (lens, i32, B), (grant, i32, B), (moves, i32, 4), moves.numel())
+    dev, B = _dev(state), cfg.B
+    _go(dev, (_lib or load()).pisa_pages_reserve, cfg, pages, _at(add, _i32, B, dev),
+        _at(state, _i32, _state_words(pages), dev), _at(table, _i32, B * -(-cfg.N // pages.S), dev),
+        _at(lens, _i32, B, dev), _at(grant, _i32, B, dev), _at(moves, _i32, 4, dev), moves.numel())
 
 
 def pisa_pages_fork(cfg, pages, parent, state, table, lens, table_out, lens_out):
     """Sequence b becomes a copy of sequence parent[b] (outside [0, B): it ends), sharing its pages."""
-    i32, B = torch.int32, cfg.B
-    n = B * pages_width(cfg, pages)
-    _paged("pisa_pages_fork", cfg, pages, (parent, i32, B), (state, i32, _state_words(pages)), (table, i32, n),
-           (lens, i32, B), (table_out, i32, n), (lens_out, i32, B))
+    dev, B = _dev(state), cfg.B
+    n = B * -(-cfg.N // pages.S)
+    _go(dev, (_lib or load()).pisa_pages_fork, cfg, pages, _at(parent, _i32, B, dev),
+        _at(state, _i32, _state_words(pages), dev), _at(table, _i32, n, dev), _at(lens, _i32, B, dev),
+        _at(table_out, _i32, n, dev), _at(lens_out, _i32, B, dev))
 
 
 def pisa_pages_free(cfg, pages, seqs, state, table, lens):
     """Ends the listed sequences."""
-    i32, B = torch.int32, cfg.B
-    _paged("pisa_pages_free", cfg, pages, (seqs, i32, 0), seqs.numel(), (state, i32, _state_words(pages)),
-           (table, i32, B * pages_width(cfg, pages)), (lens, i32, B))
+    dev, B = _dev(state), cfg.B
+    _go(dev, (_lib or load()).pisa_pages_free, cfg, pages, _at(seqs, _i32, 0, dev), seqs.numel(),
+        _at(state, _i32, _state_words(pages), dev), _at(table, _i32, B * -(-cfg.N // pages.S), dev),
+        _at(lens, _i32, B, dev))
 
 
 def pisa_pages_compact(cfg, pages, state, table, moves):
     """Moves the live pages to the low end of the pool; `moves` lists the copies to make."""
-    i32 = torch.int32
-    _paged("pisa_pages_compact", cfg, pages, (state, i32, _state_words(pages)),
-           (table, i32, cfg.B * pages_width(cfg, pages)), (moves, i32, 4), moves.numel())
+    dev = _dev(state)
+    _go(dev, (_lib or load()).pisa_pages_compact, cfg, pages, _at(state, _i32, _state_words(pages), dev),
+        _at(table, _i32, cfg.B * -(-cfg.N // pages.S), dev), _at(moves, _i32, 4, dev), moves.numel())
 
 
 def pisa_pages_copy(cfg, pages, moves, K, V):
     """Copies the pages of one layer as `moves` lists them."""
-    dt, n = _elem(cfg), _pool(cfg, pages)
-    _paged("pisa_pages_copy", cfg, pages, (moves, torch.int32, 4), moves.numel(), (K, dt, n), (V, dt, n))
+    dev, dt = _dev(moves), _elem(cfg)
+    n = pages.P * pages.S * cfg.Hkv * cfg.d
+    _go(dev, (_lib or load()).pisa_pages_copy, cfg, pages, _at(moves, _i32, 4, dev), moves.numel(), _at(K, dt, n, dev),
+        _at(V, dt, n, dev))
 
 
 def pisa_paged_append(cfg, pages, k_new, v_new, lens, count, table, K, V):
     """Writes rows k_new[b, :, i], v_new[b, :, i] ([B, Hkv, T, d], or [B, Hkv, d]), i < count[b], as the
     last count[b] of the sequence's lens[b] tokens."""
-    i32, dt, B, n = torch.int32, _elem(cfg), cfg.B, _pool(cfg, pages)
+    dev, dt, B, S = _dev(K), _elem(cfg), cfg.B, pages.S
+    row = cfg.Hkv * cfg.d
     T = k_new.shape[2] if k_new.dim() == 4 else 1
-    rows = B * cfg.Hkv * T * cfg.d
-    _paged("pisa_paged_append", cfg, pages, (k_new, dt, rows), (v_new, dt, rows), T, (lens, i32, B), (count, i32, B),
-           (table, i32, B * pages_width(cfg, pages)), (K, dt, n), (V, dt, n))
+    _go(dev, (_lib or load()).pisa_paged_append, cfg, pages, _at(k_new, dt, B * T * row, dev),
+        _at(v_new, dt, B * T * row, dev), T, _at(lens, _i32, B, dev), _at(count, _i32, B, dev),
+        _at(table, _i32, B * -(-cfg.N // S), dev), _at(K, dt, pages.P * S * row, dev), _at(V, dt, pages.P * S * row, dev))
 
 
 def pisa_paged_workspace_bytes(cfg, pages) -> int:
@@ -559,27 +566,34 @@ def alloc_paged_workspace(cfg, pages, device="cuda") -> torch.Tensor:
 
 def pisa_paged_attn(cfg, pages, q, k_new, v_new, K, V, table, lens, o, lse, ws):
     """Dense attention of one token a sequence over its paged cache (k_new, v_new given: appended on the way)."""
-    i32, dt, B, n, d = torch.int32, _elem(cfg), cfg.B, _pool(cfg, pages), cfg.d
-    _paged("pisa_paged_attn", cfg, pages, (q, dt, B * cfg.Hq * d), (k_new, dt, B * cfg.Hkv * d),
-           (v_new, dt, B * cfg.Hkv * d), (K, dt, n), (V, dt, n), (table, i32, B * pages_width(cfg, pages)),
-           (lens, i32, B), (o, dt, B * cfg.Hq * d), (lse, torch.float32, B * cfg.Hq), (ws, torch.uint8, 0), ws.numel())
+    dev, dt, B, S, d = _dev(K), _elem(cfg), cfg.B, pages.S, cfg.d
+    rows, row = B * cfg.Hq, cfg.Hkv * d
+    n = pages.P * S * row
+    _go(dev, (_lib or load()).pisa_paged_attn, cfg, pages, _at(q, dt, rows * d, dev),
+        None if k_new is None else _at(k_new, dt, B * row, dev), None if v_new is None else _at(v_new, dt, B * row, dev),
+        _at(K, dt, n, dev), _at(V, dt, n, dev), _at(table, _i32, B * -(-cfg.N // S), dev), _at(lens, _i32, B, dev),
+        _at(o, dt, rows * d, dev), None if lse is None else _at(lse, torch.float32, rows, dev),
+        _at(ws, torch.uint8, 0, dev), ws.numel())
 
 
 def pisa_paged_build_pyramid(cfg, pages, K, table, lens, pyr):
     """pisa_build_pyramid_prefix from a paged cache; sequences with lens[b] <= 0 are left untouched."""
-    i32, B = torch.int32, cfg.B
-    _paged("pisa_paged_build_pyramid", cfg, pages, (K, _elem(cfg), _pool(cfg, pages)),
-           (table, i32, B * pages_width(cfg, pages)), (lens, i32, B),
-           (pyr, torch.float32, B * cfg.Hkv * pisa_pyramid_rows(cfg) * cfg.d))
+    dev, B, S, row = _dev(K), cfg.B, pages.S, cfg.Hkv * cfg.d
+    _go(dev, (_lib or load()).pisa_paged_build_pyramid, cfg, pages, _at(K, _elem(cfg), pages.P * S * row, dev),
+        _at(table, _i32, B * -(-cfg.N // S), dev), _at(lens, _i32, B, dev),
+        _at(pyr, torch.float32, B * row * pisa_pyramid_rows(cfg), dev))
 
 
 def pisa_paged_decode_step(cfg, pages, q_new, k_new, v_new, K, V, table, lens, pyr, idx, o):
     """pisa_decode_step over a paged cache; the token in hand is token lens[b] - 1."""
-    i32, dt, B, n, d = torch.int32, _elem(cfg), cfg.B, _pool(cfg, pages), cfg.d
-    _paged("pisa_paged_decode_step", cfg, pages, (q_new, dt, B * cfg.Hq * d), (k_new, dt, B * cfg.Hkv * d),
-           (v_new, dt, B * cfg.Hkv * d), (K, dt, n), (V, dt, n), (table, i32, B * pages_width(cfg, pages)),
-           (lens, i32, B), (pyr, torch.float32, B * cfg.Hkv * pisa_pyramid_rows(cfg) * d), (idx, i32, B * cfg.Hkv * cfg.K),
-           (o, dt, B * cfg.Hq * d))
+    dev, dt, B, S, d = _dev(K), _elem(cfg), cfg.B, pages.S, cfg.d
+    heads = cfg.Hkv
+    row, qn = heads * d, B * cfg.Hq * d
+    n = pages.P * S * row
+    _go(dev, (_lib or load()).pisa_paged_decode_step, cfg, pages, _at(q_new, dt, qn, dev), _at(k_new, dt, B * row, dev),
+        _at(v_new, dt, B * row, dev), _at(K, dt, n, dev), _at(V, dt, n, dev), _at(table, _i32, B * -(-cfg.N // S), dev),
+        _at(lens, _i32, B, dev), _at(pyr, torch.float32, B * row * pisa_pyramid_rows(cfg), dev),
+        _at(idx, _i32, B * heads * cfg.K, dev), _at(o, dt, qn, dev))
 
 
 class PagedCache:

@@ -139,13 +139,12 @@ def test_binding_checks_its_tensors(lib):
         pisa.pisa_pages_init(cfg, pages, i32, i32, i32)
 
     class Fake:   # a CUDA tensor as far as the checks see
-        is_cuda, at = True, 0
+        def __init__(self, dtype, n, contiguous=True, at=0):
+            self.dtype, self.n, self.contiguous, self.at = dtype, n, contiguous, at
+            self.is_cuda = at >= 0
 
         def get_device(self):
             return self.at
-
-        def __init__(self, dtype, n, contiguous=True):
-            self.dtype, self.n, self.contiguous = dtype, n, contiguous
 
         def numel(self):
             return self.n
@@ -153,15 +152,13 @@ def test_binding_checks_its_tensors(lib):
         def is_contiguous(self):
             return self.contiguous
 
-    ok = Fake(torch.int32, 1000)
-    other = Fake(torch.int32, 1000)
-    other.at = 1
-    with pytest.raises(ValueError, match="elements"):
-        pisa._paged("pisa_pages_init", cfg, pages, (Fake(torch.int64, 1000), torch.int32, 10))
-    with pytest.raises(ValueError, match="elements"):
-        pisa._paged("pisa_pages_init", cfg, pages, (Fake(torch.int32, 9), torch.int32, 10))
-    with pytest.raises(ValueError, match="contiguous"):
-        pisa._paged("pisa_pages_init", cfg, pages, (Fake(torch.int32, 100, False), torch.int32, 10))
-    ok.data_ptr = lambda: 0
-    with pytest.raises(ValueError, match="different devices"):
-        pisa._paged("pisa_pages_init", cfg, pages, (ok, torch.int32, 1), (other, torch.int32, 1))
+        def data_ptr(self):
+            return 1 << 16
+
+    good = [Fake(torch.int32, 1000) for _ in range(3)]
+    for i in range(3):
+        for bad, text in ((Fake(torch.int64, 1000), "elements"), (Fake(torch.int32, 1), "elements"),
+                          (Fake(torch.int32, 1000, contiguous=False), "contiguous"),
+                          (Fake(torch.int32, 1000, at=1), "different devices"), (Fake(torch.int32, 1000, at=-1), "CUDA")):
+            with pytest.raises(ValueError, match=text):
+                pisa.pisa_pages_init(cfg, pages, *[bad if j == i else x for j, x in enumerate(good)])
