@@ -178,7 +178,7 @@ KERNEL_SOURCES = {
     "pool": [_CS + "pool.cu", _CS + "pisa_device.cuh"],
     "select": [_CS + "select.cu", _CS + "pisa_walk.cuh", _CS + "pisa_device.cuh"],
     "attn": [_CS + "attn.cu", _CS + "pisa_attn.cuh", _CS + "pisa_walk.cuh", _CS + "pisa_device.cuh"],
-    "decode": [_CS + "decode.cu", _CS + "tc.cuh", _CS + "pisa_walk.cuh", _CS + "pisa_device.cuh"],
+    "decode": [_CS + "decode.cu", _CS + "pisa_decode.cuh", _CS + "tc.cuh", _CS + "pisa_walk.cuh", _CS + "pisa_device.cuh"],
 }
 
 

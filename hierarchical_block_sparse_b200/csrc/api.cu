@@ -6,6 +6,7 @@
 
 #include "pisa.h"
 #include "pisa_internal.h"
+#include "pisa_paged.cuh"
 
 using namespace pisa;
 

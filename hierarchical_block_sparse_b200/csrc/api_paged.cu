@@ -175,13 +175,13 @@ int pisa_paged_build_pyramid(const pisa_cfg* cfg, const pisa_pages* pages, const
     if (!K || !table || !len || !pyr) return PISA_E_INVALID;
     if (!aligned(K, 16) || !aligned(pyr, 16) || !aligned(table, 4) || !aligned(len, 4)) return PISA_E_ALIGNMENT;
     if ((int64_t)cfg->B * cfg->Hkv > 65535) return PISA_E_UNSUPPORTED;  // one grid row per (b, kv-head)
-    PoolParams p;
+    PagedPoolParams p;
     p.B = cfg->B; p.Hkv = cfg->Hkv; p.N = cfg->N; p.C = cfg->C;
     p.k_rows = cfg->N;
     p.len = len;
     make_geom(cfg->N, cfg->C, &p.geom);
     p.table = table; p.S = pages->S; p.P = pages->P; p.W = (int)width(cfg, pages);
-    return cuda_status(launch_pool(cfg->dtype, cfg->d, K, pyr, p, (cudaStream_t)stream));
+    return cuda_status(launch_paged_pool(cfg->dtype, cfg->d, K, pyr, p, (cudaStream_t)stream));
 }
 
 int pisa_paged_decode_step(const pisa_cfg* cfg, const pisa_pages* pages, const void* q_new, const void* k_new,
@@ -196,7 +196,7 @@ int pisa_paged_decode_step(const pisa_cfg* cfg, const pisa_pages* pages, const v
     if (!aligned(q_new, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(K, 16) || !aligned(V, 16) ||
         !aligned(pyr, 16) || !aligned(o, 16) || !aligned(table, 4) || !aligned(len, 4) || !aligned(idx, 4))
         return PISA_E_ALIGNMENT;
-    DecodeParams p;
+    PagedDecodeParams p;
     p.B = cfg->B; p.Hq = cfg->Hq; p.Hkv = cfg->Hkv; p.N = cfg->N; p.C = cfg->C; p.K = cfg->K;
     p.forced_mask = cfg->forced_mask;
     p.qscale = (float)(1.4426950408889634 / sqrt((double)cfg->d));

@@ -15,7 +15,10 @@
 // The same kernel serves the paged cache (PAGED): a page holds whole leaves, so
 // a leaf's rows stay one run of memory and only its first row is looked up,
 // once, when the leaf enters the list; everything downstream is unchanged.
+#include <type_traits>
+
 #include "pisa_decode.cuh"
+#include "pisa_paged.cuh"
 #include "tc.cuh"
 
 namespace pisa {
@@ -120,12 +123,15 @@ constexpr bool decode_caches() { return G == 1; }
 template <int G>
 constexpr int decode_stages() { return decode_caches<G>() ? 2 : 3; }
 
+template <bool PAGED>
+using DecodeBlock = std::conditional_t<PAGED, PagedDecodeParams, DecodeParams>;
+
 // PAGED: Kc, Vc are the pools [P, Hkv, S, D] and `pos` holds the lengths, the new token included.
 template <typename T, int D, int G, bool PAGED>
 __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
     const T* __restrict__ q_new, T* __restrict__ Kc, T* __restrict__ Vc, float* __restrict__ pyr,
     const int32_t* __restrict__ pos, int32_t* __restrict__ idx, T* __restrict__ out, const T* __restrict__ k_new,
-    const T* __restrict__ v_new, DecodeParams p) {
+    const T* __restrict__ v_new, DecodeBlock<PAGED> p) {
     using Lo = DecLayout<T, D>;
     constexpr int NW = 8;
     constexpr int kDecStages = decode_stages<G>();
@@ -158,9 +164,12 @@ __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
     const int64_t t = PAGED ? (int64_t)pos[b] - 1 : pos[b];
     // first pool row of a leaf (pages hold whole leaves; the pool has < 2^31 rows)
     auto leaf_row = [&](int64_t leaf) -> int {
-        const int tok = (int)leaf * p.C;
-        const int page = __ldg(p.table + b * p.W + tok / p.S);
-        return (unsigned)page < (unsigned)p.P ? (page * p.Hkv + kvh) * p.S + tok % p.S : -1;
+        if constexpr (PAGED) {
+            const int tok = (int)leaf * p.C;
+            const int page = __ldg(p.table + b * p.W + tok / p.S);
+            return (unsigned)page < (unsigned)p.P ? (page * p.Hkv + kvh) * p.S + tok % p.S : -1;
+        }
+        return 0;
     };
     int new_row = 0;  // PAGED: of the new token's leaf
     if (PAGED && t >= 0 && t < p.N) new_row = leaf_row(t / p.C);
@@ -492,8 +501,8 @@ cudaError_t launch_append(int dtype, int d, void* Kc, void* Vc, float* pyr, cons
 }
 
 template <typename T, int D, int G, bool PAGED>
-static cudaError_t launch_decode_p(const void* q, void* Kc, void* Vc, float* pyr, const int32_t* pos, int32_t* idx,
-                                   void* o, const void* k_new, const void* v_new, const DecodeParams& p,
+static cudaError_t launch_decode_t(const void* q, void* Kc, void* Vc, float* pyr, const int32_t* pos, int32_t* idx,
+                                   void* o, const void* k_new, const void* v_new, const DecodeBlock<PAGED>& p,
                                    cudaStream_t st) {
     const size_t out_bytes = sizeof(float) * 8 * G * (D + 1);
     // pipeline stages + five per-warp arrays [32][8][G] of leaf states (+ the cached logits)
@@ -511,42 +520,47 @@ static cudaError_t launch_decode_p(const void* q, void* Kc, void* Vc, float* pyr
     return cudaGetLastError();
 }
 
-template <typename T, int D, int G>
-static cudaError_t launch_decode_t(const void* q, void* Kc, void* Vc, float* pyr, const int32_t* pos, int32_t* idx,
-                                   void* o, const void* k_new, const void* v_new, const DecodeParams& p,
-                                   cudaStream_t st) {
-    return p.table ? launch_decode_p<T, D, G, true>(q, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st)
-                   : launch_decode_p<T, D, G, false>(q, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
-}
-
-template <typename T, int D>
+template <typename T, int D, bool PAGED>
 static cudaError_t launch_decode_d(const void* q, void* Kc, void* Vc, float* pyr, const int32_t* pos, int32_t* idx,
-                                   void* o, const void* k_new, const void* v_new, const DecodeParams& p,
+                                   void* o, const void* k_new, const void* v_new, const DecodeBlock<PAGED>& p,
                                    cudaStream_t st) {
     switch (p.Hq / p.Hkv) {
-        case 1: return launch_decode_t<T, D, 1>(q, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
-        case 2: return launch_decode_t<T, D, 2>(q, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
-        case 4: return launch_decode_t<T, D, 4>(q, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
-        case 8: return launch_decode_t<T, D, 8>(q, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
-        case 16: return launch_decode_t<T, D, 16>(q, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
+        case 1: return launch_decode_t<T, D, 1, PAGED>(q, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
+        case 2: return launch_decode_t<T, D, 2, PAGED>(q, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
+        case 4: return launch_decode_t<T, D, 4, PAGED>(q, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
+        case 8: return launch_decode_t<T, D, 8, PAGED>(q, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
+        case 16: return launch_decode_t<T, D, 16, PAGED>(q, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+template <bool PAGED>
+static cudaError_t launch_decode_any(int dtype, int d, const void* q_new, void* Kc, void* Vc, float* pyr,
+                                     const int32_t* pos, int32_t* idx, void* o, const void* k_new, const void* v_new,
+                                     const DecodeBlock<PAGED>& p, cudaStream_t st) {
+    if (dtype == 1) {
+        if (d == 128) return launch_decode_d<__nv_bfloat16, 128, PAGED>(q_new, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
+        if (d == 64) return launch_decode_d<__nv_bfloat16, 64, PAGED>(q_new, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
+    } else {
+        if (d == 128) return launch_decode_d<float, 128, PAGED>(q_new, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
+        if (d == 64) return launch_decode_d<float, 64, PAGED>(q_new, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
     }
     return cudaErrorInvalidValue;
 }
 
 // k_new / v_new null: decode only (the row at pos was appended before);
-// otherwise the append runs inside the same kernel. With p.table, Kc and Vc are
-// the pools of a paged cache and pos holds the lengths, the new token included.
+// otherwise the append runs inside the same kernel.
 cudaError_t launch_decode(int dtype, int d, const void* q_new, void* Kc, void* Vc, float* pyr, const int32_t* pos,
                           int32_t* idx, void* o, const void* k_new, const void* v_new, const DecodeParams& p,
                           cudaStream_t st) {
-    if (dtype == 1) {
-        if (d == 128) return launch_decode_d<__nv_bfloat16, 128>(q_new, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
-        if (d == 64) return launch_decode_d<__nv_bfloat16, 64>(q_new, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
-    } else {
-        if (d == 128) return launch_decode_d<float, 128>(q_new, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
-        if (d == 64) return launch_decode_d<float, 64>(q_new, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
-    }
-    return cudaErrorInvalidValue;
+    return launch_decode_any<false>(dtype, d, q_new, Kc, Vc, pyr, pos, idx, o, k_new, v_new, p, st);
+}
+
+// Kc and Vc: the pools of a paged cache; len: the lengths, the new token included.
+cudaError_t launch_paged_decode(int dtype, int d, const void* q_new, const void* k_new, const void* v_new, void* Kc, void* Vc,
+                                const int32_t* len, float* pyr, int32_t* idx, void* o, const PagedDecodeParams& p,
+                                cudaStream_t st) {
+    return launch_decode_any<true>(dtype, d, q_new, Kc, Vc, pyr, len, idx, o, k_new, v_new, p, st);
 }
 
 }  // namespace pisa

@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps > 4 ? 1 : Tile::G <= 4 ? 4
     const typename Tile::T* __restrict__ q_new, const typename Tile::T* __restrict__ k_new,
     const typename Tile::T* __restrict__ v_new, typename Tile::T* __restrict__ K, typename Tile::T* __restrict__ V,
     const int32_t* __restrict__ len, float* __restrict__ pyr, int32_t* __restrict__ idx, typename Tile::T* __restrict__ out,
-    int z_at, DecodeParams p) {
+    int z_at, PagedDecodeParams p) {
     using T = typename Tile::T;
     constexpr int D = Tile::D, G = Tile::G, KT = Tile::KT, kThreads = kWarps * 32;
     constexpr int CPR = Tile::RowBytes / 16, RPI = 32 / CPR;
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps > 4 ? 1 : Tile::G <= 4 ? 4
 
 template <class Tile, int kWarps, int kStages>
 cudaError_t launch_shape(const void* q, const void* k_new, const void* v_new, void* K, void* V, const int32_t* len,
-                         float* pyr, int32_t* idx, void* o, const DecodeParams& p, cudaStream_t st, bool* taken) {
+                         float* pyr, int32_t* idx, void* o, const PagedDecodeParams& p, cudaStream_t st, bool* taken) {
     using T = typename Tile::T;
     const size_t smem = step_smem<Tile, kWarps, kStages>(p.C, p.K);
     // static: queries, dots, log-sum-exps; all of an SM's 227 KB at most
@@ -209,7 +209,7 @@ cudaError_t launch_shape(const void* q, const void* k_new, const void* v_new, vo
 // (G <= 4) share an SM (256 units of 8 heads at 665 tokens: 35 us, 44 with 8 warps).
 template <class Tile>
 cudaError_t launch_step(const void* q, const void* k_new, const void* v_new, void* K, void* V, const int32_t* len,
-                        float* pyr, int32_t* idx, void* o, const DecodeParams& p, cudaStream_t st, bool* taken) {
+                        float* pyr, int32_t* idx, void* o, const PagedDecodeParams& p, cudaStream_t st, bool* taken) {
     if ((int64_t)p.B * p.Hkv <= sm_count()) {
         cudaError_t e = launch_shape<Tile, 8, 3>(q, k_new, v_new, K, V, len, pyr, idx, o, p, st, taken);
         if (!*taken && e == cudaSuccess) e = launch_shape<Tile, 8, 2>(q, k_new, v_new, K, V, len, pyr, idx, o, p, st, taken);
@@ -220,7 +220,7 @@ cudaError_t launch_step(const void* q, const void* k_new, const void* v_new, voi
 
 template <int D, int G>
 cudaError_t launch_dtype(int dtype, const void* q, const void* k_new, const void* v_new, void* K, void* V,
-                         const int32_t* len, float* pyr, int32_t* idx, void* o, const DecodeParams& p, cudaStream_t st,
+                         const int32_t* len, float* pyr, int32_t* idx, void* o, const PagedDecodeParams& p, cudaStream_t st,
                          bool* taken) {
     if (dtype == 1) return launch_step<MmaTile<D, G>>(q, k_new, v_new, K, V, len, pyr, idx, o, p, st, taken);
     return launch_step<FmaTile<D, G>>(q, k_new, v_new, K, V, len, pyr, idx, o, p, st, taken);
@@ -228,7 +228,7 @@ cudaError_t launch_dtype(int dtype, const void* q, const void* k_new, const void
 
 template <int D>
 cudaError_t launch_group(int dtype, const void* q, const void* k_new, const void* v_new, void* K, void* V,
-                         const int32_t* len, float* pyr, int32_t* idx, void* o, const DecodeParams& p, cudaStream_t st,
+                         const int32_t* len, float* pyr, int32_t* idx, void* o, const PagedDecodeParams& p, cudaStream_t st,
                          bool* taken) {
     switch (p.Hq / p.Hkv) {
         case 1: return launch_dtype<D, 1>(dtype, q, k_new, v_new, K, V, len, pyr, idx, o, p, st, taken);
@@ -245,7 +245,7 @@ cudaError_t launch_group(int dtype, const void* q, const void* k_new, const void
 // The step by this kernel where its logits fit in shared memory and leaves are ranked by
 // their log-sum-exp, else by decode.cu's.
 cudaError_t launch_paged_step(int dtype, int d, const void* q, const void* k_new, const void* v_new, void* K, void* V,
-                              const int32_t* len, float* pyr, int32_t* idx, void* o, const DecodeParams& p,
+                              const int32_t* len, float* pyr, int32_t* idx, void* o, const PagedDecodeParams& p,
                               cudaStream_t st) {
     if (p.variant == PISA_SCORE_LSE) {
         bool taken = false;
@@ -253,7 +253,7 @@ cudaError_t launch_paged_step(int dtype, int d, const void* q, const void* k_new
                                        : launch_group<64>(dtype, q, k_new, v_new, K, V, len, pyr, idx, o, p, st, &taken);
         if (taken || e != cudaSuccess) return e;
     }
-    return launch_decode(dtype, d, q, K, V, pyr, len, idx, o, k_new, v_new, p, st);
+    return launch_paged_decode(dtype, d, q, k_new, v_new, K, V, len, pyr, idx, o, p, st);
 }
 
 }  // namespace pisa

@@ -16,8 +16,6 @@ struct PoolParams {
     int64_t k_rows;      // rows per head in K (N for prefill, capacity for caches)
     const int32_t* len;  // optional per-sequence key count (device), else N
     Geom geom;           // pyramid layout (for N or for the capacity)
-    const int32_t* table = nullptr;  // paged cache: K is a pool; [B, W] page ids, S tokens a page, P pages
-    int S = 0, P = 0, W = 0;
 };
 
 struct SelectParams {
@@ -37,8 +35,6 @@ struct DecodeParams {
     float qscale;  // log2(e) / sqrt(d)
     Geom geom;     // layout for the capacity N
     int variant;   // enum pisa_score
-    const int32_t* table = nullptr;  // paged cache (see PoolParams)
-    int S = 0, P = 0, W = 0;
 };
 
 // block-major tensor-core path (bf16, d = 128, C = 64)
@@ -126,29 +122,5 @@ cudaError_t launch_append(int dtype, int d, void* Kc, void* Vc, float* pyr, cons
 cudaError_t launch_decode(int dtype, int d, const void* q_new, void* Kc, void* Vc, float* pyr, const int32_t* pos,
                           int32_t* idx, void* o, const void* k_new, const void* v_new, const DecodeParams& p,
                           cudaStream_t st);
-
-// the GPU limits every call checks (api.cu): PISA_OK or the status to return
-int check_gpu_cfg(const pisa_cfg* c);
-
-// paged cache: attention (paged.cu) and the page calls (pages.cu)
-struct PagedParams;
-cudaError_t launch_paged_attn(int dtype, int d, const void* q, const void* k_new, const void* v_new, void* K, void* V,
-                              void* o, float* lse, void* ws, const PagedParams& p, int sms, cudaStream_t st);
-cudaError_t launch_paged_step(int dtype, int d, const void* q, const void* k_new, const void* v_new, void* K, void* V,
-                              const int32_t* len, float* pyr, int32_t* idx, void* o, const DecodeParams& p,
-                              cudaStream_t st);
-cudaError_t launch_paged_append(int row_bytes, const void* k_new, const void* v_new, int T, const int32_t* count, void* K,
-                                void* V, const PagedParams& p, cudaStream_t st);
-cudaError_t launch_pages_init(int32_t* state, int32_t* table, int32_t* len, int B, int P, int W, cudaStream_t st);
-cudaError_t launch_pages_reserve(const int32_t* add, int32_t* state, int32_t* table, int32_t* len, int32_t* grant,
-                                 int32_t* moves, int B, int N, int S, int P, int W, cudaStream_t st);
-cudaError_t launch_pages_fork(const int32_t* parent, int32_t* state, const int32_t* table, const int32_t* len,
-                              int32_t* table_out, int32_t* len_out, int B, int P, int W, cudaStream_t st);
-cudaError_t launch_pages_free(const int32_t* seqs, int n, int32_t* state, int32_t* table, int32_t* len, int B, int P,
-                              int W, cudaStream_t st);
-cudaError_t launch_pages_compact(int32_t* state, int32_t* table, int32_t* moves, int max_moves, int B, int P, int W,
-                                 cudaStream_t st);
-cudaError_t launch_pages_copy(const int32_t* moves, int max_moves, void* K, void* V, int64_t page_bytes, int P, int sms,
-                              cudaStream_t st);
 
 }  // namespace pisa

@@ -1,11 +1,11 @@
-// pisa_paged.cuh -- what the paged-cache kernels share: the parameter block of
-// the attention, the page state's layout and the address of a token's row.
+// pisa_paged.cuh -- what the paged-cache kernels share: their parameter blocks and
+// launchers, and the page state's layout.
 #pragma once
 
 #include <atomic>
 #include <stdint.h>
 
-#include "pisa_device.cuh"
+#include "pisa_internal.h"
 
 namespace pisa {
 
@@ -41,13 +41,20 @@ constexpr int kPagedMaxCtas = 512;
 // pages_reserve_kernel is one CTA that keeps its sequences in shared memory.
 constexpr int kReserveMaxSeqs = 4096;
 
-struct PagedParams {
-    int B, Hq, Hkv, N;     // N: most tokens a sequence holds
+struct PageView {
     int S, P, W;           // tokens a page, pages in the pool, pages a sequence
-    float qscale;          // log2(e) / sqrt(d)
     const int32_t* table;  // [B, W], -1 = no page
-    const int32_t* len;    // [B]
 };
+
+struct PagedParams : PageView {
+    int B, Hq, Hkv, N;   // N: most tokens a sequence holds
+    float qscale;        // log2(e) / sqrt(d)
+    const int32_t* len;  // [B]
+};
+
+// the contiguous kernels' blocks, K and V being pools
+struct PagedDecodeParams : DecodeParams, PageView {};
+struct PagedPoolParams : PoolParams, PageView {};
 
 // Page state, in int32 words (each part begins on a multiple of 4):
 //   refs  [P]           sequences' entries that name the page; 0 = free
@@ -66,5 +73,32 @@ struct PageState {
 
 // words in front of the (source, destination) pairs of a list of moves
 constexpr int kMovesHead = 4;
+
+// the GPU limits every call checks (api.cu): PISA_OK or the status to return
+int check_gpu_cfg(const pisa_cfg* c);
+
+cudaError_t launch_paged_attn(int dtype, int d, const void* q, const void* k_new, const void* v_new, void* K, void* V,
+                              void* o, float* lse, void* ws, const PagedParams& p, int sms, cudaStream_t st);
+cudaError_t launch_paged_append(int row_bytes, const void* k_new, const void* v_new, int T, const int32_t* count, void* K,
+                                void* V, const PagedParams& p, cudaStream_t st);
+cudaError_t launch_paged_pool(int dtype, int d, const void* K, float* pyr, const PagedPoolParams& p, cudaStream_t st);
+// the sparse step: paged_step.cu's kernel, or decode.cu's (launch_paged_decode) where that does not fit
+cudaError_t launch_paged_step(int dtype, int d, const void* q, const void* k_new, const void* v_new, void* K, void* V,
+                              const int32_t* len, float* pyr, int32_t* idx, void* o, const PagedDecodeParams& p,
+                              cudaStream_t st);
+cudaError_t launch_paged_decode(int dtype, int d, const void* q, const void* k_new, const void* v_new, void* K, void* V,
+                                const int32_t* len, float* pyr, int32_t* idx, void* o, const PagedDecodeParams& p,
+                                cudaStream_t st);
+cudaError_t launch_pages_init(int32_t* state, int32_t* table, int32_t* len, int B, int P, int W, cudaStream_t st);
+cudaError_t launch_pages_reserve(const int32_t* add, int32_t* state, int32_t* table, int32_t* len, int32_t* grant,
+                                 int32_t* moves, int B, int N, int S, int P, int W, cudaStream_t st);
+cudaError_t launch_pages_fork(const int32_t* parent, int32_t* state, const int32_t* table, const int32_t* len,
+                              int32_t* table_out, int32_t* len_out, int B, int P, int W, cudaStream_t st);
+cudaError_t launch_pages_free(const int32_t* seqs, int n, int32_t* state, int32_t* table, int32_t* len, int B, int P,
+                              int W, cudaStream_t st);
+cudaError_t launch_pages_compact(int32_t* state, int32_t* table, int32_t* moves, int max_moves, int B, int P, int W,
+                                 cudaStream_t st);
+cudaError_t launch_pages_copy(const int32_t* moves, int max_moves, void* K, void* V, int64_t page_bytes, int P, int sms,
+                              cudaStream_t st);
 
 }  // namespace pisa

@@ -5,7 +5,10 @@
 // fp32 mean, and finish the CTA's subtree (levels 2..5) in shared memory, so K
 // is read exactly once. pool_top_kernel: one CTA per head finishes the few
 // levels above (each node the mean of its existing children).
+#include <type_traits>
+
 #include "pisa_internal.h"
+#include "pisa_paged.cuh"
 
 namespace pisa {
 
@@ -21,7 +24,7 @@ __device__ __forceinline__ int64_t keys_of(const PoolParams& p, int64_t b) {
 // are one run of memory; a leaf without a page counts as zeros.
 template <typename T, int D, bool PAGED>
 __global__ void __launch_bounds__(256) pool_leaves_kernel(const T* __restrict__ K, float* __restrict__ pyr,
-                                                          PoolParams p) {
+                                                          std::conditional_t<PAGED, PagedPoolParams, PoolParams> p) {
     constexpr int E = Ld16<T>::E;   // elements per 16-byte load
     constexpr int TPR = D / E;      // lanes per row
     constexpr int RPW = 32 / TPR;   // rows per warp step
@@ -123,14 +126,11 @@ __global__ void __launch_bounds__(512) pool_top_kernel(float* __restrict__ pyr, 
     }
 }
 
-template <typename T, int D>
-static cudaError_t launch_pool_t(const void* K, float* pyr, const PoolParams& p, cudaStream_t st) {
+template <typename T, int D, typename Params>
+static cudaError_t launch_pool_t(const void* K, float* pyr, const Params& p, cudaStream_t st) {
     const int64_t M1 = p.geom.M[1];
     dim3 grid((unsigned)((M1 + kLeavesPerCta - 1) / kLeavesPerCta), (unsigned)(p.B * p.Hkv));
-    if (p.table)
-        pool_leaves_kernel<T, D, true><<<grid, 256, 0, st>>>((const T*)K, pyr, p);
-    else
-        pool_leaves_kernel<T, D, false><<<grid, 256, 0, st>>>((const T*)K, pyr, p);
+    pool_leaves_kernel<T, D, std::is_same_v<Params, PagedPoolParams>><<<grid, 256, 0, st>>>((const T*)K, pyr, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int first = 2 + 4;  // log2(kLeavesPerCta) = 4 levels above the leaves done in-CTA
@@ -197,7 +197,8 @@ cudaError_t launch_cache_grow(const void* src, void* dst, int64_t units, int64_t
     return cudaGetLastError();
 }
 
-cudaError_t launch_pool(int dtype, int d, const void* K, float* pyr, const PoolParams& p, cudaStream_t st) {
+template <typename Params>
+static cudaError_t launch_pool_any(int dtype, int d, const void* K, float* pyr, const Params& p, cudaStream_t st) {
     if (dtype == 1) {
         if (d == 128) return launch_pool_t<__nv_bfloat16, 128>(K, pyr, p, st);
         if (d == 64) return launch_pool_t<__nv_bfloat16, 64>(K, pyr, p, st);
@@ -206,6 +207,14 @@ cudaError_t launch_pool(int dtype, int d, const void* K, float* pyr, const PoolP
         if (d == 64) return launch_pool_t<float, 64>(K, pyr, p, st);
     }
     return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_pool(int dtype, int d, const void* K, float* pyr, const PoolParams& p, cudaStream_t st) {
+    return launch_pool_any(dtype, d, K, pyr, p, st);
+}
+
+cudaError_t launch_paged_pool(int dtype, int d, const void* K, float* pyr, const PagedPoolParams& p, cudaStream_t st) {
+    return launch_pool_any(dtype, d, K, pyr, p, st);
 }
 
 }  // namespace pisa
