@@ -22,7 +22,7 @@ int check(const pisa_cfg* c, const pisa_pages* g) {
     const int s = check_gpu_cfg(c);
     if (s) return s;
     if (g->S < 1 || g->P < 1) return PISA_E_INVALID;
-    if (g->S > 1024) return PISA_E_UNSUPPORTED;
+    if (g->S > 1024 || c->N > (1 << 30)) return PISA_E_UNSUPPORTED;
     if ((int64_t)g->P * c->Hkv * g->S >= ((int64_t)1 << 31)) return PISA_E_UNSUPPORTED;  // 32-bit pool rows
     if ((int64_t)c->B * width(c, g) >= ((int64_t)1 << 31)) return PISA_E_UNSUPPORTED;
     return PISA_OK;

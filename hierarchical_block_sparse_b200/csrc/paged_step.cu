@@ -36,8 +36,14 @@ size_t step_smem(int C, int K) {
     return (head + 15) / 16 * 16 + sizeof(float) * ((size_t)2 * K * Tile::G * logit_stride(C, Tile::KT) + kWarps * Tile::kWeighFloats);
 }
 
+// CTAs of one SM that the registers are cut for
+template <int G, int kWarps, int kStages>
+constexpr int step_blocks() {
+    return kWarps == 8 ? (kStages == 2 && G <= 4 ? 2 : 1) : G <= 4 ? 4 : G <= 8 ? 3 : 2;
+}
+
 template <class Tile, int kWarps, int kStages>
-__global__ void __launch_bounds__(kWarps * 32, kWarps > 4 ? 1 : Tile::G <= 4 ? 4 : Tile::G <= 8 ? 3 : 2) paged_step_kernel(
+__global__ void __launch_bounds__(kWarps * 32, step_blocks<Tile::G, kWarps, kStages>()) paged_step_kernel(
     const typename Tile::T* __restrict__ q_new, const typename Tile::T* __restrict__ k_new,
     const typename Tile::T* __restrict__ v_new, typename Tile::T* __restrict__ K, typename Tile::T* __restrict__ V,
     const int32_t* __restrict__ len, float* __restrict__ pyr, int32_t* __restrict__ idx, typename Tile::T* __restrict__ out,
@@ -205,17 +211,21 @@ cudaError_t launch_shape(const void* q, const void* k_new, const void* v_new, vo
 }
 
 // Up to one unit an SM: 8 warps and a longer ring each, for a CTA has its SM alone (64 units
-// of 4 x 8 heads at 32 K tokens: 63 us with 4 warps, 42 with 8). More units: 4 warps, so that 4
-// (G <= 4) share an SM (256 units of 8 heads at 665 tokens: 35 us, 44 with 8 warps).
+// of 4 x 8 heads at 32 K tokens: 63 us with 4 warps, 42 with 8). Up to two: 8 warps where two such
+// CTAs fit (G <= 4; 256 units at 8 K tokens: 62 us with 4 warps, 50 with 8; with groups of 8, where
+// one fits, 35 and 44 at 665 tokens). More: 4 warps, 4 CTAs (512 units: 82.5 us; 93 with 8 warps,
+// 118 with rings of 3 stages, which let 3 CTAs share an SM).
 template <class Tile>
 cudaError_t launch_step(const void* q, const void* k_new, const void* v_new, void* K, void* V, const int32_t* len,
                         float* pyr, int32_t* idx, void* o, const PagedDecodeParams& p, cudaStream_t st, bool* taken) {
-    if ((int64_t)p.B * p.Hkv <= sm_count()) {
-        cudaError_t e = launch_shape<Tile, 8, 3>(q, k_new, v_new, K, V, len, pyr, idx, o, p, st, taken);
-        if (!*taken && e == cudaSuccess) e = launch_shape<Tile, 8, 2>(q, k_new, v_new, K, V, len, pyr, idx, o, p, st, taken);
-        if (*taken || e != cudaSuccess) return e;
-    }
-    return launch_shape<Tile, 4, 2>(q, k_new, v_new, K, V, len, pyr, idx, o, p, st, taken);
+    const int64_t units = (int64_t)p.B * p.Hkv, sms = sm_count();
+    *taken = false;
+    cudaError_t e = cudaSuccess;
+    if (units <= sms) e = launch_shape<Tile, 8, 3>(q, k_new, v_new, K, V, len, pyr, idx, o, p, st, taken);
+    if (!*taken && e == cudaSuccess && units <= (Tile::G <= 4 ? 2 : 1) * sms)
+        e = launch_shape<Tile, 8, 2>(q, k_new, v_new, K, V, len, pyr, idx, o, p, st, taken);
+    if (!*taken && e == cudaSuccess) e = launch_shape<Tile, 4, 2>(q, k_new, v_new, K, V, len, pyr, idx, o, p, st, taken);
+    return e;
 }
 
 template <int D, int G>

@@ -396,7 +396,8 @@ int pisa_decode_step(const pisa_cfg *cfg, const void *q_new, const void *k_new, 
  * token whose table entry is outside [0, P) counts as absent, is not read and
  * is not written; lengths are clamped to [0, N]. A pool row past a sequence's
  * length is never used, whatever it holds (NaN included).
- * Limits: those of the decode calls, 1 <= S <= 1024, P*Hkv*S < 2^31, B*W < 2^31.
+ * Limits: those of the decode calls, N <= 2^30, 1 <= S <= 1024, P*Hkv*S < 2^31,
+ * B*W < 2^31.
  * The pyramid calls need S to be a multiple of C. */
 typedef struct pisa_pages {
     int32_t S;  /* tokens per page */

@@ -58,7 +58,7 @@ def test_refused_before_launch(lib, name):
 
     assert fn(None, pages, *args, None) == -1 and fn(_cfg(), None, *args, None) == -1
     for field, value, status in [("B", 0, -1), ("Hq", 3, -1), ("N", -1, -1), ("dtype", 9, -1), ("d", 96, -2), ("Hq", 6, -2),
-                                 ("Hq", 64, -2), ("C", 2000, -2)]:
+                                 ("Hq", 64, -2), ("C", 2000, -2), ("N", 2 ** 30 + 1, -2)]:
         cfg = _cfg()
         setattr(cfg, field, value)
         assert call(cfg) == status, (field, value)
