@@ -600,7 +600,9 @@ class PagedCache:
     """A decode cache in pages: pools K, V [P, Hkv, S, d] and, for the sparse step, a
     pyramid, for each layer; one table, lengths and page state for all of them.
     cfg.N is the most tokens a sequence may hold. No call reads device memory on
-    the host; `moves[1]` (pages missing at the last reserve) is for the caller to read."""
+    the host; `moves[1]` (pages missing at the last reserve) is for the caller to read.
+    A sequence that was granted nothing has no token in hand: `step`, and `attend` with
+    new rows, write nothing for it and give it o = 0 (idx = -1, lse = -inf)."""
 
     def __init__(self, cfg, pages, layers: int = 1, sparse: bool = True, device="cuda"):
         self.cfg, self.pages = cfg, pages
@@ -614,7 +616,7 @@ class PagedCache:
         self.state = torch.empty(pisa_pages_state_words(pages), **i32)
         self.table, self.lens = torch.empty((cfg.B, W), **i32), torch.empty(cfg.B, **i32)
         self._table, self._lens = torch.empty_like(self.table), torch.empty_like(self.lens)  # fork's other buffers
-        self.grant = torch.zeros(cfg.B, **i32)
+        self.grant, self.now = torch.zeros(cfg.B, **i32), torch.zeros(cfg.B, **i32)  # now: lens of the granted
         self.moves = torch.zeros(4 + 2 * max(cfg.B, pages.P // 2), **i32)
         self.ws = alloc_paged_workspace(cfg, pages, device)
         pisa_pages_init(cfg, pages, self.state, self.table, self.lens)
@@ -626,6 +628,7 @@ class PagedCache:
     def reserve(self, add: torch.Tensor) -> torch.Tensor:
         """Room for add[b] more tokens; returns grant (the tokens each sequence got)."""
         pisa_pages_reserve(self.cfg, self.pages, add, self.state, self.table, self.lens, self.grant, self.moves)
+        torch.mul(self.lens, self.grant > 0, out=self.now)
         self._copy()
         return self.grant
 
@@ -641,13 +644,13 @@ class PagedCache:
 
     def attend(self, q, o, lse=None, k_new=None, v_new=None, layer: int = 0) -> None:
         """Dense attention of one token a sequence (its rows appended on the way when given)."""
-        pisa_paged_attn(self.cfg, self.pages, q, k_new, v_new, self.K[layer], self.V[layer], self.table, self.lens, o, lse,
-                        self.ws)
+        pisa_paged_attn(self.cfg, self.pages, q, k_new, v_new, self.K[layer], self.V[layer], self.table,
+                        self.lens if k_new is None else self.now, o, lse, self.ws)
 
     def step(self, q_new, k_new, v_new, idx, o, layer: int = 0) -> None:
         """The sparse step (append, select, attend) for the token reserved last."""
         pisa_paged_decode_step(self.cfg, self.pages, q_new, k_new, v_new, self.K[layer], self.V[layer], self.table,
-                               self.lens, self.pyr[layer], idx, o)
+                               self.now, self.pyr[layer], idx, o)
 
     def fork(self, parent: torch.Tensor) -> None:
         """Sequence b becomes a copy of sequence parent[b]; pyramids of the new ones are rebuilt."""

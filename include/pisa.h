@@ -384,7 +384,9 @@ int pisa_decode_step(const pisa_cfg *cfg, const void *q_new, const void *k_new, 
  *   K, V:  pools [P, Hkv, S, d] of cfg->dtype: P pages of S tokens;
  *   table: int32 [B, W], W = ceil(N / S): page of tokens [w*S, (w+1)*S) of
  *          sequence b, -1 where it has none;
- *   len:   int32 [B], tokens of each sequence, those being added included;
+ *   len:   int32 [B], tokens of each sequence, those being added included (calls
+ *          that add a token take 0 for a sequence that adds none: pisa_pages_reserve
+ *          may have granted it none, and its last token would be overwritten);
  *   state: int32 [pisa_pages_state_words(pages)], 16-byte aligned: the number of
  *          table entries that name each page [P], then, from word 4*ceil(P/4) on,
  *          the bitmap of free pages (bit j of word i: page 32 i + j), then room

@@ -578,6 +578,34 @@ def test_sparse_step_without_some_leaves():
     assert bool(((o[0].cpu().double() - ro).abs() <= tol[0]).all())
 
 
+def test_a_step_without_pages_writes_nothing():
+    # the pool is full and both sequences share their last page: no grant, so no row may be written
+    cfg = pisa.make_cfg(B=2, Hq=4, Hkv=2, N=64, d=64, C=8, K=4, dtype=torch.float32)
+    c = pisa.PagedCache(cfg, pisa.make_pages(8, 3), device=DEV)
+    g = torch.Generator().manual_seed(19)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    c.reserve(torch.tensor([20, 0], **i32))
+    k, v = (torch.randn(2, 2, 20, 64, generator=g).to(DEV) for _ in range(2))
+    c.append(k, v)
+    c.fork(torch.tensor([0, 0], **i32))
+    before = [x.clone() for x in (c.K[0], c.V[0], c.pyr[0], c.table, c.lens)]
+    assert c.reserve(torch.ones(2, **i32)).tolist() == [0, 0] and int(c.moves[1]) == 1
+    q, k1, v1 = (torch.randn(2, h, 64, generator=g).to(DEV) for h in (4, 2, 2))
+    o, lse, idx = torch.ones(2, 4, 64, device=DEV), torch.ones(2, 4, device=DEV), torch.zeros(2, 2, 4, **i32)
+    c.attend(q, o, lse, k1, v1)
+    assert not o.any() and bool((lse == -math.inf).all())
+    c.step(q, k1, v1, idx, o)
+    assert not o.any() and bool((idx == -1).all())
+    for x, y in zip(before, (c.K[0], c.V[0], c.pyr[0], c.table, c.lens)):
+        assert torch.equal(x, y)
+    c.attend(q, o, lse)      # what is cached can still be attended to
+    assert bool((lse > -math.inf).all())
+    c.free(torch.tensor([1], **i32))
+    assert c.reserve(torch.tensor([1, 0], **i32)).tolist() == [1, 0]
+    c.attend(q, o, lse, k1, v1)
+    assert c.lens.tolist() == [21, 0] and bool((lse[0] > -math.inf).all()) and not o[1].any()
+
+
 # ---- as a serving program uses them ------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype,S,C", [(torch.bfloat16, 32, 16), (torch.float32, 16, 16)])
