@@ -381,17 +381,22 @@ __global__ void __launch_bounds__(1024) compact_small_kernel(int32_t* state, int
     for (int i = threadIdx.x; i < entries; i += 1024) compact_entry(table + i, live, map, P);
 }
 
-// Page data of the moves: a page of a pool is one run of bytes, cut into segments
-// of kSegment; a block takes a segment at a time, 2 x 16 bytes a thread in flight, and
-// far more blocks than fit at once even out the ends (grids of 8, 16, 64 a SM: 164, 149,
-// 143 us for 3600 pages of 128 KB, 6.6 TB/s read and written at best).
+// Page data of the moves: a page of a pool is one run of bytes, cut into segments of
+// kSegment (smaller pages are one segment). TEAM threads, as many as a segment's bytes keep
+// busy (2 KB pages with all 512: 28 us, with 64: 9, for 3660 of them), take a
+// segment at a time, up to 2 x 16 bytes a thread in flight, and far more blocks than fit at
+// once even out the ends (grids of 8, 16, 64 a SM: 164, 149, 143 us for 3600 pages of
+// 128 KB, 6.6 TB/s read and written at best).
 constexpr int kSegment = 16384;
 constexpr int kCopyThreads = 512, kCopyPer = kSegment / 16 / kCopyThreads;
+template <int TEAM>
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const int32_t* __restrict__ moves, uint8_t* __restrict__ K,
                                                          uint8_t* __restrict__ V, int64_t page_bytes, int segments, int P,
                                                          int max_moves) {
+    constexpr int kTeams = kCopyThreads / TEAM;
     const int64_t tasks = (int64_t)min(max(moves[0], 0), max_moves) * 2 * segments;
-    for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int me = threadIdx.x % TEAM, mine = kTeams == 1 ? 0 : threadIdx.x / TEAM;
+    for (int64_t task = (int64_t)blockIdx.x * kTeams + mine; task < tasks; task += (int64_t)gridDim.x * kTeams) {
         const int seg = (int)(task % segments);
         const int64_t rest = task / segments;
         const int src = moves[kMovesHead + (rest & ~(int64_t)1)], dst = moves[kMovesHead + (rest & ~(int64_t)1) + 1];
@@ -404,10 +409,10 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const int32_t*
         uint4 v[kCopyPer];
 #pragma unroll
         for (int i = 0; i < kCopyPer; ++i)
-            if (threadIdx.x + i * kCopyThreads < chunks) v[i] = __ldcs(from + threadIdx.x + i * kCopyThreads);
+            if (me + i * TEAM < chunks) v[i] = __ldcs(from + me + i * TEAM);
 #pragma unroll
         for (int i = 0; i < kCopyPer; ++i)
-            if (threadIdx.x + i * kCopyThreads < chunks) __stcs(to + threadIdx.x + i * kCopyThreads, v[i]);
+            if (me + i * TEAM < chunks) __stcs(to + me + i * TEAM, v[i]);
     }
 }
 
@@ -507,13 +512,23 @@ cudaError_t launch_pages_compact(int32_t* state, int32_t* table, int32_t* moves,
     return cudaGetLastError();
 }
 
+template <int TEAM>
+static cudaError_t launch_copy(const int32_t* moves, int max_moves, void* K, void* V, int64_t page_bytes, int P, int sms,
+                               cudaStream_t st) {
+    if constexpr (TEAM > 32)
+        if (page_bytes <= (int64_t)TEAM / 2 * kCopyPer * 16)
+            return launch_copy<TEAM / 2>(moves, max_moves, K, V, page_bytes, P, sms, st);
+    constexpr int kTeams = kCopyThreads / TEAM;
+    const int segments = (int)((page_bytes + kSegment - 1) / kSegment);
+    const int64_t want = ((int64_t)max_moves * 2 * segments + kTeams - 1) / kTeams, most = (int64_t)sms * 64;
+    pages_copy_kernel<TEAM><<<(unsigned)(want < most ? want : most), kCopyThreads, 0, st>>>(
+        moves, (uint8_t*)K, (uint8_t*)V, page_bytes, segments, P, max_moves);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_pages_copy(const int32_t* moves, int max_moves, void* K, void* V, int64_t page_bytes, int P, int sms,
                               cudaStream_t st) {
-    const int segments = (int)((page_bytes + kSegment - 1) / kSegment);
-    const int64_t want = (int64_t)max_moves * 2 * segments, most = (int64_t)sms * 64;
-    pages_copy_kernel<<<(unsigned)(want < most ? want : most), kCopyThreads, 0, st>>>(moves, (uint8_t*)K, (uint8_t*)V, page_bytes,
-                                                                             segments, P, max_moves);
-    return cudaGetLastError();
+    return launch_copy<kCopyThreads>(moves, max_moves, K, V, page_bytes, P, sms, st);
 }
 
 cudaError_t launch_paged_append(int row_bytes, const void* k_new, const void* v_new, int T, const int32_t* count, void* K,
