@@ -306,7 +306,7 @@ class Both:
 
 
 @pytest.mark.parametrize("B,N,S,P", [(6, 100, 8, 60), (33, 4000, 16, 1500), (5, 64, 1, 200), (1500, 40, 8, 5000),
-                                     (3, 30, 64, 4), (8, 300, 7, 257)])
+                                     (3, 30, 64, 4), (8, 300, 7, 257), (4096, 20, 8, 9000)])
 def test_page_calls_follow_the_model(B, N, S, P):
     r = random.Random(B)
     c = Both(B, N, S, P)
