@@ -204,10 +204,14 @@ __device__ __forceinline__ int keep_topk(int& id, float score, const LevelState&
 // the gather by rank and this keep preserve lane order, so the children
 // 2p, 2p + 1 of ascending parents ascend too): "lower index" is "lower lane",
 // and only the key crosses lanes. Invalid lanes send NaN, which ranks before
-// no one. Lanes 0..kept-1 of the result hold the kept ids in lane order;
+// no one. A score that is NaN ranks as the largest number: behind the forced
+// nodes, before all others, so that there is an order and never more than K are
+// kept (the next level's candidates and what is sized for them rely on that).
+// Lanes 0..kept-1 of the result hold the kept ids in lane order;
 // returns kept (and, if asked, the mask of kept candidate lanes).
 __device__ __forceinline__ int keep_topk_lane(int& id, float key, bool valid, int K, int lane,
                                               unsigned* kmask_out = nullptr) {
+    if (key != key) key = 3.402823466e38f;
     const float kv = valid ? key : __int_as_float(0x7fc00000);
     int before = 0;
 #pragma unroll
