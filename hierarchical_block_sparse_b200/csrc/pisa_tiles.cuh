@@ -41,10 +41,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
 
 // Byte offset of 16-byte chunk c of row r of a stage's keys (or values): runs of 128 bytes
 // of all rows one after another, chunks XOR-swizzled by the row so that the 8 rows of
@@ -62,11 +58,11 @@ __device__ __forceinline__ uint32_t ring_off(int r, int c) {
 // needs 4 G products a key element against 4 bytes of it, far below what even these
 // instructions do per byte of HBM traffic; what they cost is power, and the
 // kernel runs at the power limit.
-// P enters as bf16 high and low parts (2^-16 relative): in one rounding its error would
-// be as large as the output's own. The high part is cut, not rounded, and the low part
-// is kept above zero, so that an infinite value times both stays that infinity. With
-// G <= 4 the columns 4..7 repeat the heads 0..3 and carry the low parts, which then
-// cost nothing; larger groups take a second product.
+// P enters in three bf16 parts, 8 bits each of its 24, so that nothing of it is rounded.
+// The parts are cut, not rounded, and the lower ones kept above zero, so that an infinite
+// value times each stays that infinity. With G <= 2 the columns repeat the heads and carry
+// the three parts in one product; with G = 4 one carries the first two and another half of
+// the third twice; larger groups take three.
 template <int D_, int G_>
 struct MmaTile {
     using T = __nv_bfloat16;
@@ -75,7 +71,8 @@ struct MmaTile {
     static constexpr int RowBytes = D * 2;
     static constexpr int kScratchFloats = 0, kWeighFloats = 0;
     static constexpr int NT = G > 8 ? 2 : 1;    // column tiles
-    static constexpr bool kTwin = G <= 4;       // columns 4..7 repeat the heads for the low parts
+    static constexpr int kCols = G <= 2 ? 2 : G <= 4 ? 4 : 8;      // the heads repeat every kCols columns, a part of P each
+    static constexpr int kProducts = G <= 2 ? 1 : G <= 4 ? 2 : 3;  // that P's parts take
 
     uint32_t qb[D / 16][NT][2];
     float o[D / 16][NT][4];  // dims 16 j + g (+ 8), columns 2 c, 2 c + 1 (g = lane / 4, c = lane % 4)
@@ -92,7 +89,7 @@ struct MmaTile {
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int h = kTwin ? g & 3 : 8 * t + g, e = k * 16 + 2 * c + 8 * i;
+                    const int h = kCols < 8 ? g % kCols : 8 * t + g, e = k * 16 + 2 * c + 8 * i;
                     to[k][t][i] = h < G ? __ldg(reinterpret_cast<const unsigned*>(q + (size_t)h * D + e)) : 0u;
                 }
     }
@@ -183,7 +180,7 @@ struct MmaTile {
         }
 #pragma unroll
         for (int r = 0; r < KT / 16; ++r) {
-            uint32_t hi[NT][2], lo[NT][2];  // P^T: keys 0..7 and 8..15 of the 16
+            uint32_t pp[kProducts][NT][2];  // P^T: keys 0..7 and 8..15 of the 16
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
@@ -192,16 +189,11 @@ struct MmaTile {
                     const float p0 = ex2_approx(s[r][t][2 * i] - m0), p1 = ex2_approx(s[r][t][2 * i + 1] - m1);
                     l[t][0] += p0;
                     l[t][1] += p1;
-                    const uint32_t h = high_parts(p0, p1), w = low_parts(p0, p1);
-                    if constexpr (kTwin) {
-                        hi[t][i] = transpose8(c < 2 ? h : w);
-                    } else {
-                        hi[t][i] = transpose8(h);
-                        lo[t][i] = transpose8(w);
-                    }
+#pragma unroll
+                    for (int u = 0; u < kProducts; ++u) pp[u][t][i] = transpose8(parts(p0, p1, u, 2 * c));
                 }
             }
-            accumulate(vbuf, r, hi, lo, lane);
+            accumulate(vbuf, r, pp, lane);
         }
     }
     __device__ __forceinline__ void poison() {
@@ -236,16 +228,16 @@ struct MmaTile {
         }
     }
     // ... and o += 2^(z - Z) v over the first `rows` keys. l (its first entry) is then the sum
-    // of this lane's keys for head 8 t + lane / 4 (kTwin: (lane / 4) % 4).
+    // of this lane's keys for head 8 t + lane / 4 (where heads repeat: of that column's head).
     __device__ __forceinline__ void weigh(uint32_t vbuf, const float* z, int stride, const float* Z, int rows, int lane,
                                           float*) {
         const int g = lane >> 2, c = lane & 3;
 #pragma unroll
         for (int r = 0; r < KT / 16; ++r) {
-            uint32_t hi[NT][2], lo[NT][2];
+            uint32_t pp[kProducts][NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const int h = kTwin ? g & 3 : 8 * t + g;
+                const int h = kCols < 8 ? g % kCols : 8 * t + g;
                 const float top = h < G ? Z[h] : 0.f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -255,12 +247,11 @@ struct MmaTile {
                     const float p0 = h < G && key < rows ? ex2_approx(x.x - top) : 0.f;
                     const float p1 = h < G && key + 1 < rows ? ex2_approx(x.y - top) : 0.f;
                     l[t][0] += p0 + p1;
-                    const uint32_t u = high_parts(p0, p1), w = low_parts(p0, p1);
-                    hi[t][i] = kTwin && g >= 4 ? w : u;
-                    lo[t][i] = w;
+#pragma unroll
+                    for (int u = 0; u < kProducts; ++u) pp[u][t][i] = parts(p0, p1, u, g);
                 }
             }
-            accumulate(vbuf, r, hi, lo, lane);
+            accumulate(vbuf, r, pp, lane);
         }
     }
     // o (not yet divided) and the sums into a slot ([G][D], then [G])
@@ -279,33 +270,42 @@ struct MmaTile {
                 for (int j = 0; j < D / 16; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = o[j][t][i + 2 * e];
-                        if (kTwin) x += __shfl_xor_sync(kFull, x, 2);
-                        if (h < G && (!kTwin || c < 2)) slot[h * D + 16 * j + 8 * e + g] = x;
+                        const float x = whole(o[j][t][i + 2 * e]);
+                        if (h < G && 2 * c < kCols) slot[h * D + 16 * j + 8 * e + g] = x;
                     }
             }
         }
     }
 
-    static __device__ __forceinline__ uint32_t high_parts(float p0, float p1) {
-        return __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+    static __device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+    // what product u has of p in column `col`: its part is the first 8 bits of that (all steps are exact)
+    static __device__ __forceinline__ float share(float p, int u, int col) {
+        const int part = kProducts == 3 ? u : u == 0 ? col / kCols : 2;
+        const float r = p - cut(p), s = r - cut(r);
+        return part == 0 ? p : fmaxf(part == 1 ? r : kProducts == 2 ? 0.5f * s : s, kTiny);
     }
-    static __device__ __forceinline__ uint32_t low_parts(float p0, float p1) {
-        return pack_bf16(fmaxf(p0 - __uint_as_float(__float_as_uint(p0) & 0xffff0000u), kTiny),
-                         fmaxf(p1 - __uint_as_float(__float_as_uint(p1) & 0xffff0000u), kTiny));
+    // of two neighbouring probabilities
+    static __device__ __forceinline__ uint32_t parts(float p0, float p1, int u, int col) {
+        return __byte_perm(__float_as_uint(share(p0, u, col)), __float_as_uint(share(p1, u, col)), 0x7632);
+    }
+    // an output's columns together (of use in the lanes of the first kCols columns)
+    static __device__ __forceinline__ float whole(float x) {
+        if (kCols == 2) {
+            const float y = __shfl_xor_sync(kFull, x, 1), z = __shfl_xor_sync(kFull, x, 2);
+            return x + y + z;
+        }
+        return kCols == 4 ? x + __shfl_xor_sync(kFull, x, 2) : x;
     }
     // o += V^T P^T over keys 16 r .. 16 r + 15
-    __device__ __forceinline__ void accumulate(uint32_t vbuf, int r, const uint32_t (&hi)[NT][2], const uint32_t (&lo)[NT][2],
-                                               int lane) {
+    __device__ __forceinline__ void accumulate(uint32_t vbuf, int r, const uint32_t (&pp)[kProducts][NT][2], int lane) {
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
             uint32_t a[4];
             ldsm4_t(vbuf + ring_off<KT>(16 * r + (lane >> 4) * 8 + (lane & 7), 2 * j + ((lane >> 3) & 1)), a);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                mma16816(o[j][t], a, hi[t][0], hi[t][1]);
-                if constexpr (!kTwin) mma16816(o[j][t], a, lo[t][0], lo[t][1]);
-            }
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int u = 0; u < kProducts; ++u) mma16816(o[j][t], a, pp[u][t][0], pp[u][t][1]);
         }
     }
     // this warp's state into a merge slot ([G][D] o, then m[G], l[G]); `add`: merged with what is there
@@ -316,7 +316,7 @@ struct MmaTile {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int h = 8 * t + 2 * c + i;
-                const bool mine = h < G && (!kTwin || c < 2);
+                const bool mine = h < G && 2 * c < kCols;
                 float sum = l[t][i];
                 sum += __shfl_xor_sync(kFull, sum, 4);
                 sum += __shfl_xor_sync(kFull, sum, 8);
@@ -338,8 +338,7 @@ struct MmaTile {
                 for (int j = 0; j < D / 16; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = o[j][t][i + 2 * e];
-                        if (kTwin) x += __shfl_xor_sync(kFull, x, 2);  // the low parts' column
+                        const float x = whole(o[j][t][i + 2 * e]);
                         float* p = slot + h * D + 16 * j + 8 * e + g;
                         if (mine) *p = add ? a * x + b * *p : x;
                     }

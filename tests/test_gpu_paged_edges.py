@@ -67,3 +67,72 @@ def test_nan_leaves_rank_behind_the_forced_ones_and_no_more_than_k_are_kept(G, d
     assert torch.equal(again[3], idx[3]) and torch.equal(o2[3], o[3])
     assert torch.equal(again[2, 1], idx[2, 1]) and torch.equal(o2[2, G:], o[2, G:])
     assert bool(torch.isfinite(o2).all())
+
+
+def _dense(q, K, V, lens, N):
+    """pisa_paged_attn over keys K, V [B, Hkv, N, d], a page a sequence of 32 rows each; o and lse."""
+    B, Hkv, _, d = K.shape
+    S = 32
+    cfg = pisa.make_cfg(B=B, Hq=q.shape[1], Hkv=Hkv, N=N, d=d, C=16, K=4, dtype=q.dtype)
+    pool = [x.view(B, Hkv, N // S, S, d).transpose(1, 2).reshape(-1, Hkv, S, d).contiguous().to(DEV) for x in (K, V)]
+    pages = pisa.make_pages(S, B * N // S)
+    table = torch.arange(B * N // S, dtype=torch.int32, device=DEV).view(B, -1)
+    o, lse = torch.full_like(q, 9.0, device=DEV), torch.full(q.shape[:2], 9.0, device=DEV)
+    pisa.pisa_paged_attn(cfg, pages, q.to(DEV), None, None, *pool, table, torch.tensor(lens, dtype=torch.int32, device=DEV), o, lse,
+                         pisa.alloc_paged_workspace(cfg, pages, DEV))
+    torch.cuda.synchronize()
+    return o.cpu(), lse.cpu()
+
+
+@pytest.mark.parametrize("form", ["attention", "step"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 2, 4, 8, 16])
+def test_probabilities_keep_their_32_bits(G, d, form):
+    """Two keys with logits 0 and -x, values v0 = -p v1 to bf16: what is left of the sum shows an
+    error of p. In the unit p |v1|: a logit is one exact product, scaled (2^-24 of the scale, 2^-24 of
+    the result, 2^-24 of the difference from the maximum or the normaliser, which has 2^-22 itself),
+    |z| <= 4 in log2 units: below 2^-20 with the exponential's 2^-22. The sums have three terms of a
+    probability in parts, six additions of 2^-23: 2^-20.4. In all 2^-19 of (|v0| + p |v1|) <= 2.1 p |v1|, and half a
+    step of the result."""
+    B, N, C = 256, 64, 32
+    q = torch.zeros(B, G, d).bfloat16()
+    K, V = torch.zeros(B, 1, N, d).bfloat16(), torch.zeros(B, 1, N, d).bfloat16()
+    x = torch.arange(1, B + 1).double() / 128                 # k entries: at most 8 bits, exact
+    q[..., 0] = math.sqrt(d) if d == 64 else 11.0
+    K[:, 0, 1, 0] = (-x).bfloat16()
+    z = -x * float(q[0, 0, 0]) / math.sqrt(d)
+    p = torch.exp(z)
+    g = torch.Generator().manual_seed(41)
+    v1 = (1 + torch.randint(0, 128, (B, d), generator=g) / 128).bfloat16()
+    v0 = (-p[:, None] * v1.double()).bfloat16()
+    V[:, 0, 0], V[:, 0, 1] = v0, v1
+    if form == "attention":
+        o, _ = _dense(q, K, V, [2] * B, N)
+    else:
+        cfg = pisa.make_cfg(B=B, Hq=G, Hkv=1, N=N, d=d, C=C, K=4)
+        _, o = _step(cfg, C, q, K, V, [2] * B, True)
+    want = ((v0.double() + p[:, None] * v1.double()) / (1 + p[:, None]))[:, None].expand(B, G, d)
+    unit = (p[:, None] * v1.double() / (1 + p[:, None]))[:, None]
+    tol = torch.finfo(torch.bfloat16).eps / 2 * want.abs() + 2.1 * 2.0 ** -19 * unit
+    off = (o.double() - want).abs() / tol
+    assert float(off.max()) <= 1, float(off.max())
+
+
+@pytest.mark.parametrize("form", ["attention", "step"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("G,d", [(1, 128), (2, 64), (4, 128), (8, 64), (16, 128)])
+def test_infinite_values_that_count_stay_infinite(G, d, dtype, form):
+    # whatever bits the probability has: 1 of a single key, equal ones of two, odd ones of more
+    B, N, C = 5, 64, 16
+    g = torch.Generator().manual_seed(43)
+    q, K = torch.randn(B, G, d, generator=g).to(dtype), torch.randn(B, 1, N, d, generator=g).to(dtype)
+    K[1] = 0.0
+    V = torch.randn(B, 1, N, d, generator=g).to(dtype)
+    V[:, :, 0, 5], V[:, :, 0, 6] = math.inf, -math.inf
+    lens = [1, 2, 3, 17, 60]
+    if form == "attention":
+        o, _ = _dense(q, K, V, lens, N)
+    else:
+        _, o = _step(pisa.make_cfg(B=B, Hq=G, Hkv=1, N=N, d=d, C=C, K=4, dtype=dtype), C, q, K, V, lens, True)
+    assert bool((o[..., 5] == math.inf).all()) and bool((o[..., 6] == -math.inf).all())
+    assert bool(torch.isfinite(o[..., :5]).all()) and bool(torch.isfinite(o[..., 7:]).all())
