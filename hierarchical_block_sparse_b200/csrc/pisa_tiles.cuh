@@ -10,7 +10,6 @@ namespace pisa {
 
 constexpr int kTileBytes = 4096;
 constexpr float kRescale = 8.f;    // see softmax below
-constexpr float kTiny = 1.17549435e-38f;  // smallest normal number
 
 __device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool live) {
     const int bytes = live ? 16 : 0;  // 0: the 16 bytes become zeros, nothing is read
@@ -59,8 +58,9 @@ __device__ __forceinline__ uint32_t ring_off(int r, int c) {
 // instructions do per byte of HBM traffic; what they cost is power, and the
 // kernel runs at the power limit.
 // P enters in three bf16 parts, 8 bits each of its 24, so that nothing of it is rounded.
-// The parts are cut, not rounded, and the lower ones kept above zero, so that an infinite
-// value times each stays that infinity. With G <= 2 the columns repeat the heads and carry
+// The parts are cut, not rounded, and a lower one is never below 2^-26 of P, so that an
+// infinite value times each stays that infinity, and a P of zero adds nothing (a floor that
+// does not shrink with P would weigh values near the type's largest). With G <= 2 the columns repeat the heads and carry
 // the three parts in one product; with G = 4 one carries the first two and another half of
 // the third twice; larger groups take three.
 template <int D_, int G_>
@@ -277,12 +277,16 @@ struct MmaTile {
         }
     }
 
-    static __device__ __forceinline__ float cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+    // the first 8 bits of x, or 0
+    static __device__ __forceinline__ float cut(float x, bool any) {
+        return __uint_as_float(__float_as_uint(x) & (any ? 0xffff0000u : 0u));
+    }
     // what product u has of p in column `col`: its part is the first 8 bits of that (all steps are exact)
     static __device__ __forceinline__ float share(float p, int u, int col) {
         const int part = kProducts == 3 ? u : u == 0 ? col / kCols : 2;
-        const float r = p - cut(p), s = r - cut(r);
-        return part == 0 ? p : fmaxf(part == 1 ? r : kProducts == 2 ? 0.5f * s : s, kTiny);
+        float x = p - cut(p, part >= 1);
+        x -= cut(x, part >= 2);
+        return fmaxf(kProducts == 2 && u == 1 ? 0.5f * x : x, p * 0x1p-26f);
     }
     // of two neighbouring probabilities
     static __device__ __forceinline__ uint32_t parts(float p0, float p1, int u, int col) {

@@ -136,3 +136,25 @@ def test_infinite_values_that_count_stay_infinite(G, d, dtype, form):
         _, o = _step(pisa.make_cfg(B=B, Hq=G, Hkv=1, N=N, d=d, C=C, K=4, dtype=dtype), C, q, K, V, lens, True)
     assert bool((o[..., 5] == math.inf).all()) and bool((o[..., 6] == -math.inf).all())
     assert bool(torch.isfinite(o[..., :5]).all()) and bool(torch.isfinite(o[..., 7:]).all())
+
+
+@pytest.mark.parametrize("form", ["attention", "step"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("G,d", [(1, 128), (2, 64), (4, 128), (8, 64), (16, 128)])
+def test_keys_without_weight_add_nothing(G, d, dtype, form):
+    # keys 1, 3, 5, ...: logits 300 below the others', values near the largest of the type; e^-300 of them is nothing
+    B, N, C, n = 3, 64, 16, 50
+    g = torch.Generator().manual_seed(42)
+    q = torch.zeros(B, G, d).to(dtype)
+    q[..., 0] = math.sqrt(d) if d == 64 else 8.0
+    K, V = torch.zeros(B, 1, N, d).to(dtype), torch.randn(B, 1, N, d, generator=g).to(dtype)
+    K[:, :, 1::2, 0] = -300.0 * math.sqrt(d) / float(q[0, 0, 0])
+    V[:, :, 1::2] = 3.0e38 * torch.sign(torch.randn(B, 1, N // 2, d, generator=g)).to(dtype)
+    if form == "attention":
+        o, _ = _dense(q, K, V, [n] * B, N)
+    else:
+        _, o = _step(pisa.make_cfg(B=B, Hq=G, Hkv=1, N=N, d=d, C=C, K=4, dtype=dtype), C, q, K, V, [n] * B, True)
+    want = V[:, :, 0:n:2].double().mean(2).expand(B, G, d)
+    # 25 equal weights: the division's and the sums' roundings of 32 bits, below 2^-18 of the largest value, and the output's
+    tol = torch.finfo(dtype).eps / 2 * want.abs() + 2.0 ** -18 * V[:, :, 0:n:2].double().abs().max()
+    assert bool(((o.double() - want).abs() <= tol).all()), float((o.double() - want).abs().max())
