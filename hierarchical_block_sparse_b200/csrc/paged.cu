@@ -2,7 +2,7 @@
 //
 //   z_j = q . k_j / sqrt(d) over the len[b] cached keys;  o = sum_j e^(z_j) v_j / sum_j e^(z_j)
 //
-// One pass over the keys and values with a running maximum and sum (in log2
+// One pass over the keys and values with a running reference and sum (in log2
 // units). The work is a list of tiles of TK keys, ordered by (sequence, KV head,
 // position); CTA c takes the c-th equal share of that list, whatever the lengths, so
 // one long sequence and many short ones load the GPU alike. Beginning and ending a
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
                 const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;  // no key counted: 0
                 const float r[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
                 store_vec<T, 4>(out + (unit + hh) * D + e, r);
-                if (lse && e == 0) lse[unit + hh] = (M + log2f(sum)) * kLn2;
+                if (lse && e == 0) lse[unit + hh] = lse2(M, sum) * kLn2;
             } else {
                 // slot 0: a part that begins inside its unit; 1: one that ends inside it
                 const size_t at_part = ((size_t)cta * 2 + (t_first == 0 ? 1 : 0)) * G + hh;
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_attn_kernel(
             const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
             const float r4[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
             store_vec<T, 4>(out + (unit + hh) * D + e, r4);
-            if (lse && e == 0) lse[unit + hh] = (M + log2f(sum)) * kLn2;
+            if (lse && e == 0) lse[unit + hh] = lse2(M, sum) * kLn2;
         }
         cluster.sync();  // the others have read this CTA's part
     }
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(join_warps<G>() * 32) paged_join_kernel(T* __r
         const float r[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
         const size_t u = (size_t)item.row + hh;
         if (lane < D / 4) store_vec<T, 4>(out + u * D + lane * 4, r);
-        if (lse && lane == 0) lse[u] = (M + log2f(sum)) * kLn2;
+        if (lse && lane == 0) lse[u] = lse2(M, sum) * kLn2;
     }
 }
 

@@ -9,7 +9,13 @@
 namespace pisa {
 
 constexpr int kTileBytes = 4096;
-constexpr float kRescale = 8.f;    // see softmax below
+// A softmax's reference is set kRescale above the largest logit so far and moves only when a
+// logit passes it, so most tiles need no rescaling; terms are at most 1, and those below
+// 2^(kRescale - 126) of the largest vanish.
+constexpr float kRescale = 8.f;
+// the log-sum-exp in log2 units of terms that add up to `sum` at reference m
+__device__ __forceinline__ float lse2(float m, float sum) { return (m - kRescale) + log2f(sum * 256.f); }
+static_assert(kRescale == 8.f, "lse2 takes 2^kRescale");
 
 __device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool live) {
     const int bytes = live ? 16 : 0;  // 0: the 16 bytes become zeros, nothing is read
@@ -140,9 +146,8 @@ struct MmaTile {
                 for (int t = 0; t < NT; ++t) mma16816(s[r][t], a, qb[k][t][0], qb[k][t][1]);
             }
         }
-        // Running maximum: it is only moved when a logit passes it by more than
-        // kRescale (the terms then stay below 2^8, far from overflow), so most tiles
-        // need neither the exchange between lanes nor the rescaling of o.
+        // The reference moves when a logit passes it (see kRescale): most tiles need neither
+        // the exchange between lanes nor the rescaling of o.
         float mx[NT][2];
         bool move = false;
 #pragma unroll
@@ -156,7 +161,7 @@ struct MmaTile {
                     s[r][t][i] = live ? s[r][t][i] * qscale : -INFINITY;
                     mx[t][i & 1] = fmaxf(mx[t][i & 1], s[r][t][i]);
                 }
-            move |= mx[t][0] > m[t][0] + kRescale || mx[t][1] > m[t][1] + kRescale;
+            move |= mx[t][0] > m[t][0] || mx[t][1] > m[t][1];
         }
         if (__any_sync(kFull, move)) {
 #pragma unroll
@@ -167,7 +172,7 @@ struct MmaTile {
                     x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
                     x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
                     x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-                    const float mn = fmaxf(m[t][i], x);
+                    const float mn = x > m[t][i] ? x + kRescale : m[t][i];
                     const float a = mn == -INFINITY ? 1.f : exp2f(m[t][i] - mn);
                     m[t][i] = mn;
                     l[t][i] *= a;
@@ -497,9 +502,9 @@ struct FmaTile {
         }
 #pragma unroll
         for (int w = G; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, w));
-        const bool move = __any_sync(kFull, mx > m + kRescale);
+        const bool move = __any_sync(kFull, mx > m);
         if (move) {
-            const float mn = fmaxf(m, mx);
+            const float mn = mx > m ? mx + kRescale : m;
             const float a = mn == -INFINITY ? 1.f : exp2f(m - mn);
             m = mn;
             l *= a;

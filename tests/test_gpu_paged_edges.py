@@ -158,3 +158,22 @@ def test_keys_without_weight_add_nothing(G, d, dtype, form):
     # 25 equal weights: the division's and the sums' roundings of 32 bits, below 2^-18 of the largest value, and the output's
     tol = torch.finfo(dtype).eps / 2 * want.abs() + 2.0 ** -18 * V[:, :, 0:n:2].double().abs().max()
     assert bool(((o.double() - want).abs() <= tol).all()), float((o.double() - want).abs().max())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("G,d", [(1, 128), (2, 64), (4, 128), (8, 64), (16, 128)])
+def test_large_values_behind_growing_logits_stay_finite(G, d, dtype):
+    # a weighted mean of values of 2^120 is one of them, whatever the order in which the logits come
+    B, N = 2, 1024
+    q = torch.zeros(B, G, d).to(dtype)
+    q[..., 0] = 8.0
+    K, V = torch.zeros(B, 1, N, d).to(dtype), torch.full((B, 1, N, d), 2.0 ** 120).to(dtype)
+    K[0, :, 512:, 0] = 5.0 * math.sqrt(d) / 8.0       # 7.2 in log2 units, short of what moves the maximum at once
+    V[..., 1::2] *= -1
+    for lens in ([1024, 1024], [700, 3]):
+        o, lse = _dense(q, K, V, lens, N)
+        # the weights' sum and the weighted sum agree to the roundings of 1024 terms in 32 bits
+        assert bool(((o.double() / V[:, :, 0].double() - 1).abs() <= 2.0 ** -13 + torch.finfo(dtype).eps / 2).all())
+        z = (K[:, 0, :, 0].double() * 8.0 / math.sqrt(d))
+        for b in range(B):
+            assert float((lse[b].double() - torch.logsumexp(z[b, :lens[b]], 0)).abs().max()) <= 2.0 ** -13
