@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(kWarps * 32, step_blocks<Tile::G, kWarps, kSta
         for (int k = lane % 8; k < n; k += 8) m = fmaxf(m, zr[k]);
 #pragma unroll
         for (int w = 1; w < 8; w <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, w));
-        for (int k = lane % 8; k < n; k += 8) e += exp2f(zr[k] - m);
+        const float from = m == -INFINITY ? 0.f : m;  // keys of -inf logits alone: a sum of 0
+        for (int k = lane % 8; k < n; k += 8) e += exp2f(zr[k] - from);
 #pragma unroll
         for (int w = 1; w < 8; w <<= 1) e += __shfl_xor_sync(kFull, e, w);
         if (mine && lane % 8 == 0) s_lse[s_slot[j]][h] = n > 0 ? m + log2f(e) : -INFINITY;

@@ -177,3 +177,32 @@ def test_large_values_behind_growing_logits_stay_finite(G, d, dtype):
         z = (K[:, 0, :, 0].double() * 8.0 / math.sqrt(d))
         for b in range(B):
             assert float((lse[b].double() - torch.logsumexp(z[b, :lens[b]], 0)).abs().max()) <= 2.0 ** -13
+
+
+@pytest.mark.parametrize("paged", [False, True], ids=["contiguous", "paged"])
+@pytest.mark.parametrize("G,d,C,dtype", STEP_FORMS)
+def test_keys_of_minus_infinity_have_no_weight(G, d, C, dtype, paged):
+    # logits of -inf: a whole leaf of them, a new leaf's only key, every second key of another leaf
+    B, Hkv, K, N = 3, 2, 4, 16 * C
+    g = torch.Generator().manual_seed(33)
+    cfg = pisa.make_cfg(B=B, Hq=Hkv * G, Hkv=Hkv, N=N, d=d, C=C, K=K, dtype=dtype)
+    Kc, Vc = (torch.randn(B, Hkv, N, d, generator=g).to(dtype) for _ in range(2))
+    q = torch.randn(B, Hkv * G, d, generator=g).to(dtype)
+    q[..., 0] = 1.0
+    lens = [4 * C, 3 * C + 1, 10 * C + 1]
+    Kc[0, :, C:2 * C, 0] = -math.inf
+    Kc[1, :, 3 * C, 0] = -math.inf
+    Kc[:, :, 2 * C:3 * C:2, 0] = -math.inf
+    Kc[2, :, 5 * C:6 * C, 0] = -math.inf      # ranks last: there are better ones
+    idx, o = _step(cfg, C, q, Kc, Vc, lens, paged)
+    assert idx[0].tolist() == [[0, 1, 2, 3]] * Hkv and idx[1].tolist() == [[0, 1, 2, 3]] * Hkv and not bool((idx[2] == 5).any())
+    for b in range(B):
+        for h in range(Hkv * G):
+            pos = torch.cat([torch.arange(int(i) * C, min(int(i) * C + C, lens[b])) for i in idx[b, h // G]])
+            pos = pos[Kc[b, h // G, pos, 0] > -math.inf]
+            k, v, x = Kc[b, h // G, pos].double(), Vc[b, h // G, pos].double(), q[b, h].double()
+            want = torch.softmax((k @ x) / math.sqrt(d), 0) @ v
+            # logits: (d + 4) 2^-24 of sum |q||k|; sums of up to 4 C terms; both in numerator and denominator
+            size = float(((k.abs() @ x.abs()) / math.sqrt(d)).max())
+            tol = torch.finfo(dtype).eps / 2 * want.abs() + 2 * ((d + 4) * 2.0 ** -24 * size + 2.0 ** -17 + 4 * C * 2.0 ** -24) * v.abs().max()
+            assert bool(((o[b, h].double() - want).abs() <= tol).all()), (b, h)
