@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
             num += part[(ww * G + h) * (D + 1) + d];
             den += part[(ww * G + h) * (D + 1) + D];
         }
-        out[((b * p.Hq + (int64_t)kvh * G) * D) + i] = (T)(den > 0.f ? num / den : 0.f);
+        out[((b * p.Hq + (int64_t)kvh * G) * D) + i] = (T)(den > 0.f || den != den ? num / den : 0.f);  // NaN stays NaN; no key counted: 0
     }
 }
 

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kWarps * 32, step_blocks<Tile::G, kWarps, kSta
             num += slots[w * kSlot + i];
             den += slots[w * kSlot + G * D + i / D];
         }
-        out[head0 * D + i] = (T)(den > 0.f ? num / den : 0.f);
+        out[head0 * D + i] = (T)(den > 0.f || den != den ? num / den : 0.f);  // NaN stays NaN; no key counted: 0
     }
 }
 

@@ -180,6 +180,27 @@ def test_large_values_behind_growing_logits_stay_finite(G, d, dtype):
 
 
 @pytest.mark.parametrize("paged", [False, True], ids=["contiguous", "paged"])
+@pytest.mark.parametrize("variant", [0, 1])
+@pytest.mark.parametrize("G,d,C,dtype", STEP_FORMS)
+def test_nan_in_a_kept_leaf_is_seen(G, d, C, dtype, variant, paged):
+    B, Hkv, K, N = 3, 2, 4, 16 * C
+    g = torch.Generator().manual_seed(32)
+    cfg = pisa.make_cfg(B=B, Hq=Hkv * G, Hkv=Hkv, N=N, d=d, C=C, K=K, dtype=dtype, score_variant=variant)
+    Kc, Vc = (torch.randn(B, Hkv, N, d, generator=g).to(dtype) for _ in range(2))
+    q = torch.randn(B, Hkv * G, d, generator=g).to(dtype)
+    n = 10 * C - 1
+    Kc[0, 0, 3] = math.nan               # leaf 0 is always kept
+    Vc[1, 1, n - 2, 5] = math.nan        # and so is the current one
+    Vc[1, 1, n - 2, 6] = math.inf
+    idx, o = _step(cfg, C, q, Kc, Vc, [n] * B, paged)
+    assert bool(torch.isnan(o[0, :G]).all()) and bool(torch.isfinite(o[0, G:]).all())
+    assert bool(torch.isnan(o[1, G:, 5]).all()) and bool((o[1, G:, 6] == math.inf).all())
+    rest = torch.ones(d, dtype=torch.bool)
+    rest[5:7] = False
+    assert bool(torch.isfinite(o[1][:, rest]).all()) and bool(torch.isfinite(o[1, :G]).all()) and bool(torch.isfinite(o[2]).all())
+
+
+@pytest.mark.parametrize("paged", [False, True], ids=["contiguous", "paged"])
 @pytest.mark.parametrize("G,d,C,dtype", STEP_FORMS)
 def test_keys_of_minus_infinity_have_no_weight(G, d, C, dtype, paged):
     # logits of -inf: a whole leaf of them, a new leaf's only key, every second key of another leaf
