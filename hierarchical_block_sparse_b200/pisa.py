@@ -601,6 +601,8 @@ class PagedCache:
     pyramid, for each layer; one table, lengths and page state for all of them.
     cfg.N is the most tokens a sequence may hold. No call reads device memory on
     the host; `moves[1]` (pages missing at the last reserve) is for the caller to read.
+    Every tensor keeps its address, so graphs captured from these calls can be replayed
+    between any others, forks included.
     A sequence that was granted nothing has no token in hand: `step`, and `attend` with
     new rows, write nothing for it and give it o = 0 (idx = -1, lse = -inf)."""
 
@@ -614,8 +616,10 @@ class PagedCache:
         self.pyr = [torch.empty((cfg.B, cfg.Hkv, pisa_pyramid_rows(cfg), cfg.d), dtype=torch.float32, device=device)
                     for _ in range(layers if sparse else 0)]
         self.state = torch.empty(pisa_pages_state_words(pages), **i32)
-        self.table, self.lens = torch.empty((cfg.B, W), **i32), torch.empty(cfg.B, **i32)
-        self._table, self._lens = torch.empty_like(self.table), torch.empty_like(self.lens)  # fork's other buffers
+        # table and lengths in one buffer, which the cache keeps for life (captured graphs hold its
+        # address); fork writes the other and copies it back
+        self._ints, self._forked = torch.zeros(cfg.B * (W + 1), **i32), torch.zeros(cfg.B * (W + 1), **i32)
+        self.table, self.lens = self._ints[:cfg.B * W].view(cfg.B, W), self._ints[cfg.B * W:]
         self.grant, self.now = torch.zeros(cfg.B, **i32), torch.zeros(cfg.B, **i32)  # now: lens of the granted
         self.moves = torch.zeros(4 + 2 * max(cfg.B, pages.P // 2), **i32)
         self.ws = alloc_paged_workspace(cfg, pages, device)
@@ -654,8 +658,9 @@ class PagedCache:
 
     def fork(self, parent: torch.Tensor) -> None:
         """Sequence b becomes a copy of sequence parent[b]; pyramids of the new ones are rebuilt."""
-        pisa_pages_fork(self.cfg, self.pages, parent, self.state, self.table, self.lens, self._table, self._lens)
-        self.table, self._table, self.lens, self._lens = self._table, self.table, self._lens, self.lens
+        n = self.table.numel()
+        pisa_pages_fork(self.cfg, self.pages, parent, self.state, self.table, self.lens, self._forked[:n], self._forked[n:])
+        self._ints.copy_(self._forked)
         if self.pyr:
             same = parent == torch.arange(self.cfg.B, dtype=torch.int32, device=parent.device)
             lens = self.lens.masked_fill(same, 0)

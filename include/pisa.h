@@ -430,8 +430,10 @@ int pisa_pages_reserve(const pisa_cfg *cfg, const pisa_pages *pages, const int32
 /* Sequence b becomes a copy of sequence parent[b] (int32 [B]; b itself: it stays;
  * outside [0, B): it ends), for all b at once, so parents may be repeated,
  * swapped or chained. table_out [B, W] and len_out [B] are written; table and len
- * are the old ones, to be given up. Pages are shared, not copied (see
- * pisa_pages_reserve); pages that no sequence names any more become free.
+ * are the old ones, to be given up: no call may use them any more, a replayed graph
+ * neither (copy the new ones back into them where graphs hold their addresses).
+ * Pages are shared, not copied (see pisa_pages_reserve); pages that no sequence
+ * names any more become free.
  * table_out == table or len_out == len gives PISA_E_INVALID. */
 int pisa_pages_fork(const pisa_cfg *cfg, const pisa_pages *pages, const int32_t *parent, int32_t *state,
                     const int32_t *table, const int32_t *len, int32_t *table_out, int32_t *len_out, void *stream);
