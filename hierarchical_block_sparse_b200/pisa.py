@@ -603,8 +603,9 @@ class PagedCache:
     the host; `moves[1]` (pages missing at the last reserve) is for the caller to read.
     Every tensor keeps its address, so graphs captured from these calls can be replayed
     between any others, forks included.
-    A sequence that was granted nothing has no token in hand: `step`, and `attend` with
-    new rows, write nothing for it and give it o = 0 (idx = -1, lse = -inf)."""
+    A sequence that was granted nothing at the last reserve, or was forked or freed since, has
+    no token in hand: `step`, and `attend` with new rows, write nothing for it and give it
+    o = 0 (idx = -1, lse = -inf)."""
 
     def __init__(self, cfg, pages, layers: int = 1, sparse: bool = True, device="cuda"):
         self.cfg, self.pages = cfg, pages
@@ -620,7 +621,8 @@ class PagedCache:
         # address); fork writes the other and copies it back
         self._ints, self._forked = torch.zeros(cfg.B * (W + 1), **i32), torch.zeros(cfg.B * (W + 1), **i32)
         self.table, self.lens = self._ints[:cfg.B * W].view(cfg.B, W), self._ints[cfg.B * W:]
-        self.grant, self.now = torch.zeros(cfg.B, **i32), torch.zeros(cfg.B, **i32)  # now: lens of the granted
+        self._hand = torch.zeros((2, cfg.B), **i32)
+        self.grant, self.now = self._hand  # the tokens granted last; lens of the sequences that got some, else 0
         self.moves = torch.zeros(4 + 2 * max(cfg.B, pages.P // 2), **i32)
         self.ws = alloc_paged_workspace(cfg, pages, device)
         pisa_pages_init(cfg, pages, self.state, self.table, self.lens)
@@ -657,10 +659,12 @@ class PagedCache:
                                self.now, self.pyr[layer], idx, o)
 
     def fork(self, parent: torch.Tensor) -> None:
-        """Sequence b becomes a copy of sequence parent[b]; pyramids of the new ones are rebuilt."""
+        """Sequence b becomes a copy of sequence parent[b]; pyramids of the new ones are rebuilt.
+        No sequence has a token in hand then: rows are written again behind the next reserve."""
         n = self.table.numel()
         pisa_pages_fork(self.cfg, self.pages, parent, self.state, self.table, self.lens, self._forked[:n], self._forked[n:])
         self._ints.copy_(self._forked)
+        self._hand.zero_()
         if self.pyr:
             same = parent == torch.arange(self.cfg.B, dtype=torch.int32, device=parent.device)
             lens = self.lens.masked_fill(same, 0)

@@ -155,3 +155,59 @@ def test_captured_steps_go_on_across_forks(N, S, dtype):
             c.compact()
             story.m.compact()
     assert seen > 40
+
+
+def test_nothing_is_in_hand_behind_a_fork():
+    # rows may be written again once a reserve has given room: the forked rows' pages are shared
+    c, story = _make(3, 256, 16, 60)
+    g = torch.Generator().manual_seed(53)
+    lens = [40, 5, 23]
+    c.reserve(torch.tensor(lens, **I32))
+    story.m.reserve(lens)
+    k, v = (torch.randn(3, 2, 40, 64, generator=g).bfloat16() for _ in range(2))
+    c.append(k.to(DEV), v.to(DEV))
+    c.build_pyramid()
+    for b in range(3):
+        story.add(b, [k[b, :, :lens[b]], v[b, :, :lens[b]]])
+    for parent in ([0, 0, 2], [1, 0, -1]):
+        c.fork(torch.tensor(parent, **I32))
+        story.fork(parent)
+        before = [x.clone() for x in (c.K[0], c.V[0], c.pyr[0])]
+        q, k1, v1 = (torch.randn(3, h, 64, generator=g).bfloat16().to(DEV) for h in (4, 2, 2))
+        o, lse, idx = torch.ones(3, 4, 64, device=DEV).bfloat16(), torch.ones(3, 4, device=DEV), torch.zeros(3, 2, 4, **I32)
+        c.step(q, k1, v1, idx, o)
+        assert not o.any() and bool((idx == -1).all())
+        o.fill_(1)
+        c.attend(q, o, lse, k1, v1)
+        assert not o.any() and bool((lse == -math.inf).all())
+        c.append(k1, v1)
+        c.append(torch.randn(3, 2, 50, 64, generator=g).bfloat16().to(DEV), torch.randn(3, 2, 50, 64, generator=g).bfloat16().to(DEV))
+        story.check()
+        for x, y in zip(before, (c.K[0], c.V[0], c.pyr[0])):
+            assert torch.equal(x.float().nan_to_num(5.0), y.float().nan_to_num(5.0))
+    c.reserve(torch.tensor([1, 0, 0], **I32))
+    c.step(q, k1, v1, idx, o)
+    assert bool((idx[0, :, 0] == 0).all()) and bool((idx[1:] == -1).all())
+
+
+def test_freed_sequences_have_nothing_in_hand():
+    # and those that go on keep their token
+    c, story = _make(3, 256, 16, 60)
+    g = torch.Generator().manual_seed(54)
+    k, v = (torch.randn(3, 2, 30, 64, generator=g).bfloat16() for _ in range(2))
+    c.reserve(torch.tensor([30, 20, 10], **I32))
+    c.append(k.to(DEV), v.to(DEV))
+    c.build_pyramid()
+    c.reserve(torch.tensor([1, 1, 1], **I32))
+    c.free(torch.tensor([0, 0, 7], **I32))
+    before = [x.clone() for x in (c.K[0], c.V[0], c.pyr[0])]
+    q, k1, v1 = (torch.randn(3, h, 64, generator=g).bfloat16().to(DEV) for h in (4, 2, 2))
+    o, lse, idx = torch.ones(3, 4, 64, device=DEV).bfloat16(), torch.ones(3, 4, device=DEV), torch.zeros(3, 2, 4, **I32)
+    c.step(q, k1, v1, idx, o)
+    assert not o[0].any() and bool((idx[0] == -1).all()) and bool((idx[1:, :, 0] == 0).all())
+    c.attend(q, o, lse, k1, v1)
+    assert not o[0].any() and bool((lse[0] == -math.inf).all()) and bool((lse[1:] > -math.inf).all())
+    c.append(k1, v1)
+    changed = (c.K[0] != before[0]).any(-1).any(1).nonzero().tolist()
+    assert sorted(changed) == sorted([[int(c.table[b, (n - 1) // 16]), (n - 1) % 16] for b, n in ((1, 21), (2, 11))])
+    assert torch.equal(c.pyr[0][0].nan_to_num(5.0), before[2][0].nan_to_num(5.0))
