@@ -38,6 +38,17 @@ PagedParams params(const pisa_cfg* c, const pisa_pages* g, const int32_t* table,
     return p;
 }
 
+PagedDecodeParams decode_params(const pisa_cfg* c, const pisa_pages* g, const int32_t* table) {
+    PagedDecodeParams p;
+    p.B = c->B; p.Hq = c->Hq; p.Hkv = c->Hkv; p.N = c->N; p.C = c->C; p.K = c->K;
+    p.forced_mask = c->forced_mask;
+    p.qscale = (float)(1.4426950408889634 / sqrt((double)c->d));
+    make_geom(c->N, c->C, &p.geom);
+    p.variant = c->score_variant;
+    p.table = table; p.S = g->S; p.P = g->P; p.W = (int)width(c, g);
+    return p;
+}
+
 int elem_bytes(const pisa_cfg* c) { return c->dtype == PISA_DTYPE_BF16 ? 2 : 4; }
 
 }  // namespace
@@ -184,6 +195,20 @@ int pisa_paged_build_pyramid(const pisa_cfg* cfg, const pisa_pages* pages, const
     return cuda_status(launch_paged_pool(cfg->dtype, cfg->d, K, pyr, p, (cudaStream_t)stream));
 }
 
+int pisa_paged_pyramid_append(const pisa_cfg* cfg, const pisa_pages* pages, const void* k_new, const void* v_new, void* K,
+                              void* V, const int32_t* table, const int32_t* len, float* pyr, void* stream) {
+    const int s = check(cfg, pages);
+    if (s) return s;
+    if (pages->S % cfg->C != 0) return PISA_E_UNSUPPORTED;
+    if (cfg->N == 0) return PISA_OK;
+    if (!k_new || !v_new || !K || !V || K == V || !table || !len || !pyr) return PISA_E_INVALID;
+    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(pyr, 16) ||
+        !aligned(table, 4) || !aligned(len, 4))
+        return PISA_E_ALIGNMENT;
+    return cuda_status(launch_paged_pyramid_append(cfg->dtype, cfg->d, K, V, pyr, k_new, v_new, len,
+                                                   decode_params(cfg, pages, table), (cudaStream_t)stream));
+}
+
 int pisa_paged_decode_step(const pisa_cfg* cfg, const pisa_pages* pages, const void* q_new, const void* k_new,
                            const void* v_new, void* K, void* V, const int32_t* table, const int32_t* len, float* pyr,
                            int32_t* idx, void* o, void* stream) {
@@ -196,15 +221,8 @@ int pisa_paged_decode_step(const pisa_cfg* cfg, const pisa_pages* pages, const v
     if (!aligned(q_new, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(K, 16) || !aligned(V, 16) ||
         !aligned(pyr, 16) || !aligned(o, 16) || !aligned(table, 4) || !aligned(len, 4) || !aligned(idx, 4))
         return PISA_E_ALIGNMENT;
-    PagedDecodeParams p;
-    p.B = cfg->B; p.Hq = cfg->Hq; p.Hkv = cfg->Hkv; p.N = cfg->N; p.C = cfg->C; p.K = cfg->K;
-    p.forced_mask = cfg->forced_mask;
-    p.qscale = (float)(1.4426950408889634 / sqrt((double)cfg->d));
-    make_geom(cfg->N, cfg->C, &p.geom);
-    p.variant = cfg->score_variant;
-    p.table = table; p.S = pages->S; p.P = pages->P; p.W = (int)width(cfg, pages);
-    return cuda_status(launch_paged_step(cfg->dtype, cfg->d, q_new, k_new, v_new, K, V, len, pyr, idx, o, p,
-                                         (cudaStream_t)stream));
+    return cuda_status(launch_paged_step(cfg->dtype, cfg->d, q_new, k_new, v_new, K, V, len, pyr, idx, o,
+                                         decode_params(cfg, pages, table), (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -23,17 +23,26 @@
 
 namespace pisa {
 
-template <typename T, int D>
+template <bool PAGED>
+using DecodeBlock = std::conditional_t<PAGED, PagedDecodeParams, DecodeParams>;
+
+// PAGED, here and below: Kc, Vc are the pools [P, Hkv, S, D] and `pos` holds the lengths, the new token included.
+template <typename T, int D, bool PAGED>
 __global__ void __launch_bounds__(128) append_kernel(T* __restrict__ Kc, T* __restrict__ Vc,
                                                      float* __restrict__ pyr, const T* __restrict__ k_new,
                                                      const T* __restrict__ v_new, const int32_t* __restrict__ pos,
-                                                     DecodeParams p) {
+                                                     DecodeBlock<PAGED> p) {
     __shared__ __align__(16) float scratch[(4 + kMaxLevels) * D];
     const int64_t unit = blockIdx.x;  // b * Hkv + kvh
     const int64_t b = unit / p.Hkv;
-    const int64_t n = pos[b];
+    const int64_t n = PAGED ? (int64_t)pos[b] - 1 : pos[b];
     if (n < 0 || n >= p.N) return;
-    const int64_t row = unit * p.N + n / p.C * p.C;  // the leaf's first
+    int64_t row = unit * p.N + n / p.C * p.C;  // the leaf's first
+    if constexpr (PAGED) {
+        const int tok = (int)(n / p.C) * p.C, page = __ldg(p.table + b * p.W + tok / p.S);
+        if ((unsigned)page >= (unsigned)p.P) return;
+        row = ((int64_t)page * p.Hkv + unit % p.Hkv) * p.S + tok % p.S;
+    }
     append_unit<T, D, 4>(Kc + row * D, Vc + row * D, pyr + unit * p.geom.rows * D, k_new + unit * D,
                          v_new + unit * D, n, p, threadIdx.x >> 5, threadIdx.x & 31, scratch, 0);
 }
@@ -123,10 +132,6 @@ constexpr bool decode_caches() { return G == 1; }
 template <int G>
 constexpr int decode_stages() { return decode_caches<G>() ? 2 : 3; }
 
-template <bool PAGED>
-using DecodeBlock = std::conditional_t<PAGED, PagedDecodeParams, DecodeParams>;
-
-// PAGED: Kc, Vc are the pools [P, Hkv, S, D] and `pos` holds the lengths, the new token included.
 template <typename T, int D, int G, bool PAGED>
 __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
     const T* __restrict__ q_new, T* __restrict__ Kc, T* __restrict__ Vc, float* __restrict__ pyr,
@@ -479,25 +484,36 @@ __global__ void __launch_bounds__(256, decode_min_blocks<G>()) decode_kernel(
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool PAGED>
 static cudaError_t launch_append_t(void* Kc, void* Vc, float* pyr, const void* k_new, const void* v_new,
-                                   const int32_t* pos, const DecodeParams& p, cudaStream_t st) {
+                                   const int32_t* pos, const DecodeBlock<PAGED>& p, cudaStream_t st) {
     const int64_t units = (int64_t)p.B * p.Hkv;
-    append_kernel<T, D><<<(unsigned)units, 128, 0, st>>>((T*)Kc, (T*)Vc, pyr, (const T*)k_new, (const T*)v_new,
-                                                          pos, p);
+    append_kernel<T, D, PAGED><<<(unsigned)units, 128, 0, st>>>((T*)Kc, (T*)Vc, pyr, (const T*)k_new, (const T*)v_new,
+                                                                 pos, p);
     return cudaGetLastError();
+}
+
+template <bool PAGED>
+static cudaError_t launch_append_any(int dtype, int d, void* Kc, void* Vc, float* pyr, const void* k_new, const void* v_new,
+                                     const int32_t* pos, const DecodeBlock<PAGED>& p, cudaStream_t st) {
+    if (dtype == 1) {
+        if (d == 128) return launch_append_t<__nv_bfloat16, 128, PAGED>(Kc, Vc, pyr, k_new, v_new, pos, p, st);
+        if (d == 64) return launch_append_t<__nv_bfloat16, 64, PAGED>(Kc, Vc, pyr, k_new, v_new, pos, p, st);
+    } else {
+        if (d == 128) return launch_append_t<float, 128, PAGED>(Kc, Vc, pyr, k_new, v_new, pos, p, st);
+        if (d == 64) return launch_append_t<float, 64, PAGED>(Kc, Vc, pyr, k_new, v_new, pos, p, st);
+    }
+    return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_append(int dtype, int d, void* Kc, void* Vc, float* pyr, const void* k_new, const void* v_new,
                           const int32_t* pos, const DecodeParams& p, cudaStream_t st) {
-    if (dtype == 1) {
-        if (d == 128) return launch_append_t<__nv_bfloat16, 128>(Kc, Vc, pyr, k_new, v_new, pos, p, st);
-        if (d == 64) return launch_append_t<__nv_bfloat16, 64>(Kc, Vc, pyr, k_new, v_new, pos, p, st);
-    } else {
-        if (d == 128) return launch_append_t<float, 128>(Kc, Vc, pyr, k_new, v_new, pos, p, st);
-        if (d == 64) return launch_append_t<float, 64>(Kc, Vc, pyr, k_new, v_new, pos, p, st);
-    }
-    return cudaErrorInvalidValue;
+    return launch_append_any<false>(dtype, d, Kc, Vc, pyr, k_new, v_new, pos, p, st);
+}
+
+cudaError_t launch_paged_pyramid_append(int dtype, int d, void* K, void* V, float* pyr, const void* k_new, const void* v_new,
+                                        const int32_t* len, const PagedDecodeParams& p, cudaStream_t st) {
+    return launch_append_any<true>(dtype, d, K, V, pyr, k_new, v_new, len, p, st);
 }
 
 template <typename T, int D, int G, bool PAGED>

@@ -89,6 +89,8 @@ cudaError_t launch_paged_step(int dtype, int d, const void* q, const void* k_new
 cudaError_t launch_paged_decode(int dtype, int d, const void* q, const void* k_new, const void* v_new, void* K, void* V,
                                 const int32_t* len, float* pyr, int32_t* idx, void* o, const PagedDecodeParams& p,
                                 cudaStream_t st);
+cudaError_t launch_paged_pyramid_append(int dtype, int d, void* K, void* V, float* pyr, const void* k_new, const void* v_new,
+                                        const int32_t* len, const PagedDecodeParams& p, cudaStream_t st);
 cudaError_t launch_pages_init(int32_t* state, int32_t* table, int32_t* len, int B, int P, int W, cudaStream_t st);
 cudaError_t launch_pages_reserve(const int32_t* add, int32_t* state, int32_t* table, int32_t* len, int32_t* grant,
                                  int32_t* moves, int B, int N, int S, int P, int W, cudaStream_t st);

@@ -112,6 +112,7 @@ def load(path: str | None = None):
             "pisa_paged_workspace_bytes": (I64, [cfgp, pgp]),
             "pisa_paged_attn": (ctypes.c_int, [cfgp, pgp, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]),
             "pisa_paged_build_pyramid": (ctypes.c_int, [cfgp, pgp, P, P, P, P, P]),
+            "pisa_paged_pyramid_append": (ctypes.c_int, [cfgp, pgp, P, P, P, P, P, P, P, P]),
             "pisa_paged_decode_step": (ctypes.c_int, [cfgp, pgp, P, P, P, P, P, P, P, P, P, P, P]),
             "pisa_fma_probe": (ctypes.c_int, [P, ctypes.c_int, ctypes.c_int, ctypes.c_int, P]),
             "pisa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -584,6 +585,15 @@ def pisa_paged_build_pyramid(cfg, pages, K, table, lens, pyr):
         _at(pyr, torch.float32, B * row * pisa_pyramid_rows(cfg), dev))
 
 
+def pisa_paged_pyramid_append(cfg, pages, k_new, v_new, K, V, table, lens, pyr):
+    """One token's rows into the pages (token lens[b] - 1) and into the summaries."""
+    dev, dt, B, S, row = _dev(K), _elem(cfg), cfg.B, pages.S, cfg.Hkv * cfg.d
+    n = pages.P * S * row
+    _go(dev, (_lib or load()).pisa_paged_pyramid_append, cfg, pages, _at(k_new, dt, B * row, dev), _at(v_new, dt, B * row, dev),
+        _at(K, dt, n, dev), _at(V, dt, n, dev), _at(table, _i32, B * -(-cfg.N // S), dev), _at(lens, _i32, B, dev),
+        _at(pyr, torch.float32, B * row * pisa_pyramid_rows(cfg), dev))
+
+
 def pisa_paged_decode_step(cfg, pages, q_new, k_new, v_new, K, V, table, lens, pyr, idx, o):
     """pisa_decode_step over a paged cache; the token in hand is token lens[b] - 1."""
     dev, dt, B, S, d = _dev(K), _elem(cfg), cfg.B, pages.S, cfg.d
@@ -605,7 +615,10 @@ class PagedCache:
     between any others, forks included.
     A sequence that was granted nothing at the last reserve, or was forked or freed since, has
     no token in hand: `step`, and `attend` with new rows, write nothing for it and give it
-    o = 0 (idx = -1, lse = -inf)."""
+    o = 0 (idx = -1, lse = -inf).
+    A sparse cache whose pages hold whole leaves (S % C == 0) keeps the summaries of every layer
+    with all that is written, so a layer's tokens may be attended densely at first and sparsely later
+    (layers that never step are better kept in a cache with sparse=False: one launch less a token)."""
 
     def __init__(self, cfg, pages, layers: int = 1, sparse: bool = True, device="cuda"):
         self.cfg, self.pages = cfg, pages
@@ -616,6 +629,7 @@ class PagedCache:
         self.V = [torch.empty(shape, dtype=dt, device=device) for _ in range(layers)]
         self.pyr = [torch.empty((cfg.B, cfg.Hkv, pisa_pyramid_rows(cfg), cfg.d), dtype=torch.float32, device=device)
                     for _ in range(layers if sparse else 0)]
+        self._sums = sparse and pages.S % cfg.C == 0   # pages hold whole leaves: there are summaries to keep
         self.state = torch.empty(pisa_pages_state_words(pages), **i32)
         # table and lengths in one buffer, which the cache keeps for life (captured graphs hold its
         # address); fork writes the other and copies it back
@@ -639,17 +653,32 @@ class PagedCache:
         return self.grant
 
     def append(self, k_new, v_new, layer: int = 0, count: torch.Tensor | None = None) -> None:
-        """Rows of the tokens granted last (or of `count`) into the pages."""
-        pisa_paged_append(self.cfg, self.pages, k_new, v_new, self.lens, self.grant if count is None else count,
-                          self.table, self.K[layer], self.V[layer])
+        """Rows of the tokens granted last (or of `count`) into the pages. A sparse cache's summaries
+        follow: of one token in its own leaf and ancestors, of several by a build of the sequences that got them."""
+        count = self.grant if count is None else count
+        T = k_new.shape[2] if k_new.dim() == 4 else 1
+        if self._sums and T == 1:
+            pisa_paged_pyramid_append(self.cfg, self.pages, k_new, v_new, self.K[layer], self.V[layer], self.table,
+                                      self.lens * (count == 1), self.pyr[layer])
+            return
+        pisa_paged_append(self.cfg, self.pages, k_new, v_new, self.lens, count, self.table, self.K[layer], self.V[layer])
+        if self._sums and T > 1:
+            self.build_pyramid(layer, self.lens * ((count > 0) & (count <= T)))
 
     def build_pyramid(self, layer: int = 0, lens: torch.Tensor | None = None) -> None:
-        """Summaries of what is cached (or of lens[b] tokens; <= 0: left as they are)."""
+        """Summaries of what is cached (or of lens[b] tokens; <= 0: left as they are, so `now` means the
+        sequences of the last reserve). The other calls keep them; rows written past the class need this."""
         pisa_paged_build_pyramid(self.cfg, self.pages, self.K[layer], self.table, self.lens if lens is None else lens,
                                  self.pyr[layer])
 
     def attend(self, q, o, lse=None, k_new=None, v_new=None, layer: int = 0) -> None:
-        """Dense attention of one token a sequence (its rows appended on the way when given)."""
+        """Dense attention of one token a sequence (its rows appended on the way when given; a sparse
+        cache's summaries follow, so that steps can)."""
+        if self._sums and k_new is not None and v_new is not None:
+            pisa_paged_pyramid_append(self.cfg, self.pages, k_new, v_new, self.K[layer], self.V[layer], self.table, self.now,
+                                      self.pyr[layer])
+            pisa_paged_attn(self.cfg, self.pages, q, None, None, self.K[layer], self.V[layer], self.table, self.now, o, lse, self.ws)
+            return
         pisa_paged_attn(self.cfg, self.pages, q, k_new, v_new, self.K[layer], self.V[layer], self.table,
                         self.lens if k_new is None else self.now, o, lse, self.ws)
 
@@ -665,7 +694,7 @@ class PagedCache:
         pisa_pages_fork(self.cfg, self.pages, parent, self.state, self.table, self.lens, self._forked[:n], self._forked[n:])
         self._ints.copy_(self._forked)
         self._hand.zero_()
-        if self.pyr:
+        if self._sums:
             same = parent == torch.arange(self.cfg.B, dtype=torch.int32, device=parent.device)
             lens = self.lens.masked_fill(same, 0)
             for layer in range(len(self.pyr)):

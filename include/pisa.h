@@ -460,7 +460,9 @@ int pisa_pages_copy(const pisa_cfg *cfg, const pisa_pages *pages, const int32_t 
 /* Writes the last count[b] (int32 [B]) of each sequence's len[b] tokens into its
  * pages: rows k_new[b, :, i], v_new[b, :, i] ([B, Hkv, T, d], the layout of the
  * prefill's K and V), i < count[b], are tokens len[b] - count[b] + i. A count
- * outside [0, min(T, len[b])], or a length past N, leaves the sequence untouched. */
+ * outside [0, min(T, len[b])], or a length past N, leaves the sequence untouched.
+ * Summaries stay as they are: pisa_paged_build_pyramid, or pisa_paged_pyramid_append for
+ * each token, is due before the layer's next pisa_paged_decode_step. */
 int pisa_paged_append(const pisa_cfg *cfg, const pisa_pages *pages, const void *k_new, const void *v_new, int T,
                       const int32_t *len, const int32_t *count, const int32_t *table, void *K, void *V, void *stream);
 
@@ -475,7 +477,9 @@ int64_t pisa_paged_workspace_bytes(const pisa_cfg *cfg, const pisa_pages *pages)
  * (written; may be NULL), the natural log of the sum of exponentials. A
  * sequence without keys gives o = 0, lse = -inf. With k_new, v_new ([B, Hkv, d];
  * both or neither) the token len[b] - 1 is written into its page on the way, as
- * pisa_paged_append with T = 1 and count 1 would. C, K, g, forced_mask and score_variant
+ * pisa_paged_append with T = 1 and count 1 would; summaries stay as they are (a layer that
+ * is to be attended sparsely later takes its tokens by pisa_paged_pyramid_append, and this
+ * call without them). C, K, g, forced_mask and score_variant
  * do not matter. B*Hkv*(N/32 + 2) >= 2^31 gives PISA_E_UNSUPPORTED. Equal inputs give
  * equal bits. A wait for a copy that takes over
  * about a second is given up; the sequences it concerns get NaN. workspace: 16-byte aligned,
@@ -492,8 +496,17 @@ int pisa_paged_attn(const pisa_cfg *cfg, const pisa_pages *pages, const void *q,
 int pisa_paged_build_pyramid(const pisa_cfg *cfg, const pisa_pages *pages, const void *K, const int32_t *table,
                              const int32_t *len, float *pyr, void *stream);
 
+/* pisa_pyramid_append over a paged cache, in the same kernel: k_new, v_new [B, Hkv, d] become
+ * token len[b] - 1 of each sequence, and the summaries that hold it are recomputed from the
+ * leaf's rows and its ancestors' other children (those of the tokens before it have to be
+ * there). A sequence with len[b] outside [1, N], or without a page for the token, is left
+ * untouched. S % C != 0 gives PISA_E_UNSUPPORTED. */
+int pisa_paged_pyramid_append(const pisa_cfg *cfg, const pisa_pages *pages, const void *k_new, const void *v_new, void *K,
+                              void *V, const int32_t *table, const int32_t *len, float *pyr, void *stream);
+
 /* pisa_decode_step over a paged cache: the same kernel and results, the token
- * being token len[b] - 1 (pos = len - 1). A sequence with len[b] outside [1, N], or
+ * being token len[b] - 1 (pos = len - 1); pyr holds the summaries of the tokens before it.
+ * A sequence with len[b] outside [1, N], or
  * without a page for the token, gets idx = -1 and o = 0 and is left untouched.
  * S % C != 0 gives PISA_E_UNSUPPORTED. */
 int pisa_paged_decode_step(const pisa_cfg *cfg, const pisa_pages *pages, const void *q_new, const void *k_new,

@@ -211,3 +211,123 @@ def test_freed_sequences_have_nothing_in_hand():
     changed = (c.K[0] != before[0]).any(-1).any(1).nonzero().tolist()
     assert sorted(changed) == sorted([[int(c.table[b, (n - 1) // 16]), (n - 1) % 16] for b, n in ((1, 21), (2, 11))])
     assert torch.equal(c.pyr[0][0].nan_to_num(5.0), before[2][0].nan_to_num(5.0))
+
+
+@pytest.mark.parametrize("C,S,d,dtype", [(16, 48, 64, torch.float32), (64, 64, 128, torch.bfloat16), (7, 14, 64, torch.bfloat16)])
+def test_one_token_s_summaries_are_the_contiguous_cache_s(C, S, d, dtype):
+    B, Hkv, N = 6, 2, 700
+    g = torch.Generator().manual_seed(56)
+    cfg = pisa.make_cfg(B=B, Hq=Hkv, Hkv=Hkv, N=N, d=d, C=C, K=4, dtype=dtype)
+    W = -(-N // S)
+    pages = pisa.make_pages(S, B * W + 3)
+    table = torch.randperm(B * W + 3, generator=g)[:B * W].view(B, W).int().to(DEV)
+    n = torch.tensor([0, 1, C, 333, N - 3, C - 1], **I32)
+    Kc, Vc = (torch.randn(B, Hkv, N, d, generator=g).to(dtype).to(DEV) for _ in range(2))
+    Kp, Vp = (torch.zeros(B * W + 3, Hkv, S, d, dtype=dtype, device=DEV) for _ in range(2))
+    pisa.pisa_paged_append(cfg, pages, Kc, Vc, n, n, table, Kp, Vp)
+    pyr = torch.zeros(B, Hkv, pisa.pisa_pyramid_rows(cfg), d, device=DEV)
+    pisa.pisa_build_pyramid_prefix(cfg, Kc, n, pyr)
+    pyp = pyr.clone()
+    for _ in range(3):
+        k, v = (torch.randn(B, Hkv, d, generator=g).to(dtype).to(DEV) for _ in range(2))
+        pisa.pisa_pyramid_append(cfg, Kc, Vc, pyr, k, v, n)
+        n = n + 1
+        pisa.pisa_paged_pyramid_append(cfg, pages, k, v, Kp, Vp, table, n, pyp)
+        assert torch.equal(pyr, pyp)
+    for b in range(B):
+        pos = torch.arange(int(n[b]), device=DEV)
+        for c, p in ((Kc, Kp), (Vc, Vp)):
+            assert torch.equal(p[table[b].long()[pos // S], :, pos % S].transpose(0, 1), c[b, :, :int(n[b])])
+    # no token, past the capacity, no page: untouched
+    before = [x.clone() for x in (Kp, Vp, pyp)]
+    table[3, (int(n[3]) - 1) // S] = pages.P
+    pisa.pisa_paged_pyramid_append(cfg, pages, k, v, Kp, Vp, table, torch.tensor([0, -4, N + 1, int(n[3]), 0, 2 ** 31 - 1], **I32), pyp)
+    for x, y in zip(before, (Kp, Vp, pyp)):
+        assert torch.equal(x, y)
+
+
+def test_a_sparse_cache_of_pages_that_split_leaves_still_serves_densely():
+    # there are no summaries to keep: append, attention and forks work, a step is refused
+    c, story = _make(2, 256, 24, 40)
+    g = torch.Generator().manual_seed(57)
+    k, v = (torch.randn(2, 2, 30, 64, generator=g).bfloat16() for _ in range(2))
+    c.reserve(torch.tensor([30, 7], **I32))
+    story.m.reserve([30, 7])
+    c.append(k.to(DEV), v.to(DEV))
+    for b, n in enumerate((30, 7)):
+        story.add(b, [k[b, :, :n], v[b, :, :n]])
+    c.fork(torch.tensor([0, 0], **I32))
+    story.fork([0, 0])
+    c.reserve(torch.ones(2, **I32))
+    story.m.reserve([1, 1])
+    q, k1, v1 = (torch.randn(2, h, 64, generator=g).bfloat16() for h in (4, 2, 2))
+    o, lse = torch.ones(2, 4, 64, device=DEV).bfloat16(), torch.ones(2, 4, device=DEV)
+    c.attend(q.to(DEV), o, lse, k1.to(DEV), v1.to(DEV))
+    for b in range(2):
+        story.add(b, [k1[b][:, None], v1[b][:, None]])
+    story.check()
+    story.check_dense(0, q, o, lse, story.m.lens)
+    with pytest.raises(pisa.PisaError) as e:
+        c.step(q.to(DEV), k1.to(DEV), v1.to(DEV), torch.zeros(2, 2, 4, **I32), o)
+    assert e.value.status == -2
+
+
+@pytest.mark.parametrize("N,S,C,d,G,dtype", [(512, 32, 16, 64, 2, torch.bfloat16), (8192, 64, 32, 128, 4, torch.bfloat16),
+                                             (4096, 48, 16, 64, 1, torch.float32)])
+def test_a_layer_takes_dense_tokens_and_then_sparse_steps(N, S, C, d, G, dtype):
+    """Short sequences are attended in full, longer ones sparsely: the summaries have to be there."""
+    B, Hkv, K = 4, 2, 4
+    g = torch.Generator().manual_seed(55)
+    c, story = _make(B, N, S, 150, C=C, K=K, d=d, G=G, dtype=dtype)
+    one = torch.ones(B, **I32)
+
+    def rnd(*shape):
+        return torch.randn(*shape, generator=g).to(dtype)
+
+    def token(sparse):
+        q, k, v = rnd(B, Hkv * G, d), rnd(B, Hkv, d), rnd(B, Hkv, d)
+        grant = c.reserve(one).tolist()
+        story.m.reserve([1] * B)
+        for b in range(B):
+            if grant[b]:
+                story.add(b, [k[b][:, None], v[b][:, None]])
+        o, lse, idx = torch.empty(B, Hkv * G, d, dtype=dtype, device=DEV), torch.empty(B, Hkv * G, device=DEV), torch.empty(B, Hkv, K, **I32)
+        if sparse:
+            c.step(q.to(DEV), k.to(DEV), v.to(DEV), idx, o)
+        else:
+            c.attend(q.to(DEV), o, lse, k.to(DEV), v.to(DEV))
+        return q, idx, o, lse
+
+    def prompt(add, T):
+        k, v = rnd(B, Hkv, T, d), rnd(B, Hkv, T, d)
+        c.reserve(torch.tensor(add, **I32))
+        story.m.reserve(add)
+        c.append(k.to(DEV), v.to(DEV))
+        for b in range(B):
+            story.add(b, [k[b, :, :add[b]], v[b, :, :add[b]]])
+
+    seen = 0
+    prompt([3 * C + 1, 0, 1, 9 * C], 9 * C)
+    for _ in range(3):
+        for _ in range(2 * C + 3):
+            q, _, o, lse = token(False)
+        story.check()
+        story.check_dense(0, q, o, lse, story.m.lens)
+        for _ in range(2):
+            q, idx, o, _ = token(True)
+            seen += story.check_sparse(0, q, idx.cpu(), o.cpu())
+        # several rows behind what is there, by a count of the caller's; then a sparse step at once
+        prompt([0, 5, 3 * C, 1], 3 * C)
+        q, idx, o, _ = token(True)
+        seen += story.check_sparse(0, q, idx.cpu(), o.cpu())
+        # a token by append alone
+        k, v = rnd(B, Hkv, d), rnd(B, Hkv, d)
+        c.reserve(one)
+        story.m.reserve([1] * B)
+        c.append(k.to(DEV), v.to(DEV))
+        for b in range(B):
+            story.add(b, [k[b][:, None], v[b][:, None]])
+        q, idx, o, _ = token(True)
+        seen += story.check_sparse(0, q, idx.cpu(), o.cpu())
+        story.check()
+    assert seen > 40
