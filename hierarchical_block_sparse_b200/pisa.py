@@ -542,12 +542,20 @@ def pisa_pages_copy(cfg, pages, moves, K, V):
         _at(V, dt, n, dev))
 
 
+def _new_rows(k_new, v_new) -> int:
+    """T: rows a sequence that are to be appended."""
+    T = k_new.shape[2] if k_new.dim() == 4 else 1
+    if v_new.dim() == 4 and v_new.shape[2] != T:
+        raise ValueError(f"k_new and v_new differ in rows a sequence ({T}, {v_new.shape[2]})")
+    return T
+
+
 def pisa_paged_append(cfg, pages, k_new, v_new, lens, count, table, K, V):
     """Writes rows k_new[b, :, i], v_new[b, :, i] ([B, Hkv, T, d], or [B, Hkv, d]), i < count[b], as the
     last count[b] of the sequence's lens[b] tokens."""
     dev, dt, B, S = _dev(K), _elem(cfg), cfg.B, pages.S
     row = cfg.Hkv * cfg.d
-    T = k_new.shape[2] if k_new.dim() == 4 else 1
+    T = _new_rows(k_new, v_new)
     _go(dev, (_lib or load()).pisa_paged_append, cfg, pages, _at(k_new, dt, B * T * row, dev),
         _at(v_new, dt, B * T * row, dev), T, _at(lens, _i32, B, dev), _at(count, _i32, B, dev),
         _at(table, _i32, B * -(-cfg.N // S), dev), _at(K, dt, pages.P * S * row, dev), _at(V, dt, pages.P * S * row, dev))
@@ -656,7 +664,7 @@ class PagedCache:
         """Rows of the tokens granted last (or of `count`) into the pages. A sparse cache's summaries
         follow: of one token in its own leaf and ancestors, of several by a build of the sequences that got them."""
         count = self.grant if count is None else count
-        T = k_new.shape[2] if k_new.dim() == 4 else 1
+        T = _new_rows(k_new, v_new)
         if self._sums and T == 1:
             pisa_paged_pyramid_append(self.cfg, self.pages, k_new, v_new, self.K[layer], self.V[layer], self.table,
                                       self.lens * (count == 1), self.pyr[layer])
