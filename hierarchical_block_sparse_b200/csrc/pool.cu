@@ -21,7 +21,7 @@ __device__ __forceinline__ int64_t keys_of(const PoolParams& p, int64_t b) {
 }
 
 // PAGED: K is a pool [P, Hkv, S, D] whose pages hold whole leaves, so a leaf's rows
-// are one run of memory; a leaf without a page counts as zeros.
+// are one run of memory; a leaf without a page counts as zero keys, in its ancestors' means too.
 template <typename T, int D, bool PAGED>
 __global__ void __launch_bounds__(256) pool_leaves_kernel(const T* __restrict__ K, float* __restrict__ pyr,
                                                           std::conditional_t<PAGED, PagedPoolParams, PoolParams> p) {

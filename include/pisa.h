@@ -491,7 +491,9 @@ int pisa_paged_attn(const pisa_cfg *cfg, const pisa_pages *pages, const void *q,
 
 /* pisa_build_pyramid_prefix from a paged cache: summaries of the first len[b]
  * tokens, laid out for N. Sequences with len[b] <= 0 are left untouched (so a
- * forked sequence's pyramid can be built alone). S % C != 0 gives
+ * forked sequence's pyramid can be built alone). A leaf without a page counts as
+ * zero keys here: its summary is 0 and enters its ancestors' means as such (no page
+ * call leaves such a hole; a step gives the leaf itself no weight). S % C != 0 gives
  * PISA_E_UNSUPPORTED. */
 int pisa_paged_build_pyramid(const pisa_cfg *cfg, const pisa_pages *pages, const void *K, const int32_t *table,
                              const int32_t *len, float *pyr, void *stream);

@@ -246,6 +246,33 @@ def test_one_token_s_summaries_are_the_contiguous_cache_s(C, S, d, dtype):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("C,S,d,dtype", [(16, 32, 64, torch.float32), (64, 64, 128, torch.bfloat16)])
+def test_summaries_count_absent_leaves_as_zero_keys(C, S, d, dtype):
+    B, Hkv, N = 3, 2, 40 * C
+    g = torch.Generator().manual_seed(58)
+    cfg = pisa.make_cfg(B=B, Hq=Hkv, Hkv=Hkv, N=N, d=d, C=C, K=4, dtype=dtype)
+    W = -(-N // S)
+    P = B * W + 3
+    table = torch.randperm(P, generator=g)[:B * W].view(B, W).int()
+    K = torch.randn(P, Hkv, S, d, generator=g).to(dtype)
+    lens = [33 * C + 5, 7 * C, 9]
+    table[0, 3], table[0, 8], table[0, (lens[0] - 1) // S], table[1, 0], table[2] = -1, P, -2000000000, 10 ** 9, -1
+    pyr = torch.full((B, Hkv, pisa.pisa_pyramid_rows(cfg), d), math.nan, device=DEV)
+    pisa.pisa_paged_build_pyramid(cfg, pisa.make_pages(S, P), K.to(DEV), table.to(DEV), torch.tensor(lens, **I32), pyr)
+    pyr = pyr.cpu().double()
+    for b in range(B):
+        pos = torch.arange(lens[b])
+        page = table[b].long()[pos // S]
+        x = K[page.clamp(0, P - 1), :, pos % S].double().masked_fill(((page < 0) | (page >= P))[:, None, None], 0.0).transpose(0, 1)
+        x = torch.stack([x[:, i:i + C].mean(1) for i in range(0, lens[b], C)], 1)
+        for level in range(1, pisa.pisa_num_levels(cfg) + 1):
+            at = pisa.pisa_level_offset(cfg, level)
+            got = pyr[b, :, at:at + x.shape[1]]
+            # a mean of C rows in 32 bits, and a halving a level above: C + level roundings of 2^-24 of the largest key
+            assert float((got - x).abs().max()) <= (C + level) * 2.0 ** -24 * 6, (b, level)
+            x = torch.stack([x[:, i:i + 2].mean(1) for i in range(0, x.shape[1], 2)], 1)
+
+
 def test_a_sparse_cache_of_pages_that_split_leaves_still_serves_densely():
     # there are no summaries to keep: append, attention and forks work, a step is refused
     c, story = _make(2, 256, 24, 40)
