@@ -243,7 +243,7 @@ __device__ __forceinline__ int keep_leaves(int cand, int64_t n_keys, int64_t t, 
         float e = x == -INFINITY ? 0.f : exp2f(x - m);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) e += __shfl_xor_sync(kFull, e, o);
-        if (lane == 0) s_Z[h] = m + log2f(e);
+        if (lane == 0) s_Z[h] = e == 0.f ? INFINITY : m + log2f(e);  // logits of -inf alone: no key has weight
     }
     return out_id;
 }

@@ -200,6 +200,25 @@ def test_nan_in_a_kept_leaf_is_seen(G, d, C, dtype, variant, paged):
     assert bool(torch.isfinite(o[1][:, rest]).all()) and bool(torch.isfinite(o[1, :G]).all()) and bool(torch.isfinite(o[2]).all())
 
 
+@pytest.mark.parametrize("form", ["contiguous", "paged", "attention"])
+@pytest.mark.parametrize("G,d,C,dtype", STEP_FORMS)
+def test_nothing_but_keys_of_minus_infinity_gives_0(G, d, C, dtype, form):
+    # as for a sequence without keys: no key has any weight
+    B, N = 3, 16 * C
+    g = torch.Generator().manual_seed(34)
+    Kc, Vc = (torch.randn(B, 1, N, d, generator=g).to(dtype) for _ in range(2))
+    q = torch.randn(B, G, d, generator=g).to(dtype)
+    q[..., 0] = 1.0
+    Kc[:2, :, :, 0] = -math.inf
+    lens = [1, 9 * C + 2, 9 * C + 2]
+    if form == "attention":
+        o, lse = _dense(q, Kc, Vc, lens, N)
+        assert bool((lse[:2] == -math.inf).all())
+    else:
+        _, o = _step(pisa.make_cfg(B=B, Hq=G, Hkv=1, N=N, d=d, C=C, K=4, dtype=dtype), C, q, Kc, Vc, lens, form == "paged")
+    assert not bool(o[:2].any()) and bool(torch.isfinite(o[2]).all()) and bool(o[2].any())
+
+
 @pytest.mark.parametrize("paged", [False, True], ids=["contiguous", "paged"])
 @pytest.mark.parametrize("G,d,C,dtype", STEP_FORMS)
 def test_keys_of_minus_infinity_have_no_weight(G, d, C, dtype, paged):
