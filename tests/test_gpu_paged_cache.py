@@ -157,6 +157,48 @@ def test_captured_steps_go_on_across_forks(N, S, dtype):
     assert seen > 40
 
 
+def test_a_captured_turn_with_its_fork_and_compaction():
+    # everything of a beam step in one graph, replayed; eager calls in between
+    B, N, S, P = 4, 512, 16, 130
+    g, r = torch.Generator().manual_seed(59), random.Random(60)
+    c, story = _make(B, N, S, P)
+    lens = [50, 9, 17, 1]
+    c.reserve(torch.tensor(lens, **I32))
+    story.m.reserve(lens)
+    k, v = (torch.randn(B, 2, 50, 64, generator=g).bfloat16() for _ in range(2))
+    c.append(k.to(DEV), v.to(DEV))
+    for b in range(B):
+        story.add(b, [k[b, :, :lens[b]], v[b, :, :lens[b]]])
+    parent, one = torch.arange(B, **I32), torch.ones(B, **I32)
+    q, k1, v1 = (torch.zeros(B, h, 64, device=DEV).bfloat16() for h in (4, 2, 2))
+    idx, o = torch.empty(B, 2, 4, **I32), torch.empty_like(q)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.fork(parent)
+        c.compact()
+        c.reserve(one)
+        c.step(q, k1, v1, idx, o)
+    story.check()
+    for turn in range(8):
+        p = [r.choice([b, r.randrange(B)]) for b in range(B)]
+        parent.copy_(torch.tensor(p, dtype=torch.int32))
+        for t in (q, k1, v1):
+            t.copy_(torch.randn(t.shape, generator=g).bfloat16())
+        graph.replay()
+        story.fork(p)
+        story.m.compact()
+        story.m.reserve([1] * B)
+        for b in range(B):
+            story.add(b, [k1[b].cpu()[:, None], v1[b].cpu()[:, None]])
+        story.check()
+        story.check_sparse(0, q.cpu(), idx.cpu(), o.cpu())
+        if turn == 4:
+            c.free(torch.tensor([2], **I32))
+            story.m.free([2])
+            story.rows[2] = story.empty()
+
+
 def test_nothing_is_in_hand_behind_a_fork():
     # rows may be written again once a reserve has given room: the forked rows' pages are shared
     c, story = _make(3, 256, 16, 60)
