@@ -438,11 +438,6 @@ def pages_width(cfg, pages) -> int:
     return -(-cfg.N // pages.S)
 
 
-def _state_words(pages):
-    P = pages.P
-    return 2 * (P + 3 & ~3) + 3 * ((P + 31) // 32 + 3 & ~3) + 16
-
-
 def pisa_pages_state_words(pages) -> int:
     r = int(load().pisa_pages_state_words(ctypes.byref(pages)))
     if r < 0:
