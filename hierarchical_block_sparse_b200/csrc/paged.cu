@@ -611,7 +611,7 @@ cudaError_t launch_tile(const void* q, const void* k_new, const void* v_new, voi
     cfg.gridDim = dim3((unsigned)grid, Tile::G);
     cfg.blockDim = dim3(join_warps<Tile::G>() * 32);
     cfg.stream = st;
-    cudaLaunchAttribute attr;  // the join's launch and its look at the lengths overlap the kernel above
+    cudaLaunchAttribute attr;  // the join's launch overlaps the kernel above
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;

@@ -481,7 +481,7 @@ int64_t pisa_paged_workspace_bytes(const pisa_cfg *cfg, const pisa_pages *pages)
  * is to be attended sparsely later takes its tokens by pisa_paged_pyramid_append, and this
  * call without them). C, K, g, forced_mask and score_variant
  * do not matter. B*Hkv*(N/32 + 2) >= 2^31 gives PISA_E_UNSUPPORTED. Equal inputs give
- * equal bits. A wait for a copy that takes over
+ * equal bits. Keys of -inf logits alone count as none. A wait for a copy that takes over
  * about a second is given up; the sequences it concerns get NaN. workspace: 16-byte aligned,
  * contents arbitrary, nothing is kept in it; calls that share one must not
  * overlap on the GPU. */
@@ -506,10 +506,12 @@ int pisa_paged_build_pyramid(const pisa_cfg *cfg, const pisa_pages *pages, const
 int pisa_paged_pyramid_append(const pisa_cfg *cfg, const pisa_pages *pages, const void *k_new, const void *v_new, void *K,
                               void *V, const int32_t *table, const int32_t *len, float *pyr, void *stream);
 
-/* pisa_decode_step over a paged cache: the same kernel and results, the token
+/* pisa_decode_step over a paged cache: the same formulas and rule of selection, the token
  * being token len[b] - 1 (pos = len - 1); pyr holds the summaries of the tokens before it.
- * A sequence with len[b] outside [1, N], or
- * without a page for the token, gets idx = -1 and o = 0 and is left untouched.
+ * Sums are taken in another order (a kernel of its own, except for the PISA-1 and PISA-2
+ * scores and leaves whose logits do not fit in shared memory), so results agree to 32-bit
+ * roundings and scores that tie to them may fall either way. A sequence with len[b] outside
+ * [1, N], or without a page for the token, gets idx = -1 and o = 0 and is left untouched.
  * S % C != 0 gives PISA_E_UNSUPPORTED. */
 int pisa_paged_decode_step(const pisa_cfg *cfg, const pisa_pages *pages, const void *q_new, const void *k_new,
                            const void *v_new, void *K, void *V, const int32_t *table, const int32_t *len, float *pyr,
