@@ -118,6 +118,32 @@ def test_probabilities_keep_their_32_bits(G, d, form):
     assert float(off.max()) <= 1, float(off.max())
 
 
+@pytest.mark.parametrize("G,d", [(1, 128), (2, 64), (4, 128), (8, 128), (8, 64), (16, 128)])
+def test_long_sums_are_rounded_not_cut(G, d):
+    """The same odd weights with values v in one half of 256 K keys and -v in the other: the output is 0.
+    600 units keep one unit's keys in one block of 4 warps. In the unit v = 255 / 128: a tile's product
+    may be cut in each of at most 3 parts (3 * 2^-23), and a warp adds 4096 tiles, partial sums at most half
+    of its weights: roundings of 2^-24 of that, independent, so of deviation 64 * 2^-25 / sqrt(3) = 1.1e-6;
+    six of it are 6.6e-6 a warp, 3.3e-6 for the mean of four, and 0.4e-6 for the cuts. Cuts in every addition
+    alike would be 4096 / 2 * 2^-24 / 4 = 3e-5."""
+    B, N, Hkv, S = 300, 262144, 2, 64
+    cfg = pisa.make_cfg(B=B, Hq=Hkv * G, Hkv=Hkv, N=N, d=d, C=64, K=16)
+    pages = pisa.make_pages(S, N // S)
+    g = torch.Generator().manual_seed(44)
+    w = torch.randn(N // 2, generator=g)
+    K, V = torch.zeros(N, d), torch.full((N, d), 255 / 128)
+    K[:, 0] = torch.cat([w, w])
+    V[N // 2:] *= -1
+    pool = [x.bfloat16().view(N // S, 1, S, d).expand(-1, Hkv, -1, -1).contiguous().to(DEV) for x in (K, V)]
+    table = torch.arange(N // S, dtype=torch.int32, device=DEV).expand(B, -1).contiguous()
+    q = torch.zeros(B, Hkv * G, d, device=DEV).bfloat16()
+    q[..., 0] = 5.0
+    o = torch.empty_like(q)
+    pisa.pisa_paged_attn(cfg, pages, q, None, None, *pool, table, torch.full((B,), N, dtype=torch.int32, device=DEV), o, None,
+                         pisa.alloc_paged_workspace(cfg, pages, DEV))
+    assert float(o.float().abs().max()) <= 3.7e-6 * 255 / 128, float(o.float().abs().max())
+
+
 @pytest.mark.parametrize("form", ["attention", "step"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("G,d", [(1, 128), (2, 64), (4, 128), (8, 64), (16, 128)])
