@@ -660,13 +660,17 @@ class PagedCache:
         follow: of one token in its own leaf and ancestors, of several by a build of the sequences that got them."""
         count = self.grant if count is None else count
         T = _new_rows(k_new, v_new)
+        if self._sums and T > 0:
+            _at(count, _i32, self.cfg.B, self.lens.get_device())
+            first = count.view(-1)[:self.cfg.B]
+            lens = self.lens * ((first > 0) & (first <= T))   # of the sequences that get rows
         if self._sums and T == 1:
-            pisa_paged_pyramid_append(self.cfg, self.pages, k_new, v_new, self.K[layer], self.V[layer], self.table,
-                                      self.lens * (count == 1), self.pyr[layer])
+            pisa_paged_pyramid_append(self.cfg, self.pages, k_new, v_new, self.K[layer], self.V[layer], self.table, lens,
+                                      self.pyr[layer])
             return
         pisa_paged_append(self.cfg, self.pages, k_new, v_new, self.lens, count, self.table, self.K[layer], self.V[layer])
         if self._sums and T > 1:
-            self.build_pyramid(layer, self.lens * ((count > 0) & (count <= T)))
+            self.build_pyramid(layer, lens)
 
     def build_pyramid(self, layer: int = 0, lens: torch.Tensor | None = None) -> None:
         """Summaries of what is cached (or of lens[b] tokens; <= 0: left as they are, so `now` means the

@@ -157,6 +157,33 @@ def test_captured_steps_go_on_across_forks(N, S, dtype):
     assert seen > 40
 
 
+def test_counts_of_an_append_are_checked_and_may_be_longer():
+    c, story = _make(2, 256, 16, 40)
+    g = torch.Generator().manual_seed(63)
+    c.reserve(torch.tensor([20, 30], **I32))
+    story.m.reserve([20, 30])
+    k, v = (torch.randn(2, 2, 30, 64, generator=g).bfloat16() for _ in range(2))
+    for T in (1, 30):
+        for bad in (torch.ones(2, dtype=torch.int64, device=DEV), torch.ones(1, **I32), torch.ones(2, dtype=torch.int32), torch.ones(4, **I32)[::2]):
+            with pytest.raises(ValueError):
+                c.append(k[:, :, :T].contiguous().to(DEV), v[:, :, :T].contiguous().to(DEV), count=bad)
+    c.append(k.to(DEV), v.to(DEV), count=torch.tensor([20, 30, 7, 7], **I32))
+    for b, n in enumerate((20, 30)):
+        story.add(b, [k[b, :, :n], v[b, :, :n]])
+    c.reserve(torch.ones(2, **I32))
+    story.m.reserve([1, 1])
+    k1, v1 = (torch.randn(2, 2, 64, generator=g).bfloat16() for _ in range(2))
+    c.append(k1.to(DEV), v1.to(DEV), count=torch.tensor([1, 1, 0], **I32))
+    for b in range(2):
+        story.add(b, [k1[b][:, None], v1[b][:, None]])
+    story.check()
+    pyr = c.pyr[0].clone()
+    c.build_pyramid()
+    live = [(b, n) for b, n in enumerate(story.m.lens)]
+    for b, n in live:   # level 1: means of at most 16 rows in 32 bits
+        assert float((c.pyr[0][b, :, :-(-n // 16)] - pyr[b, :, :-(-n // 16)]).abs().max()) <= 16 * 2.0 ** -24 * 8
+
+
 def test_a_captured_turn_with_its_fork_and_compaction():
     # everything of a beam step in one graph, replayed; eager calls in between
     B, N, S, P = 4, 512, 16, 130
