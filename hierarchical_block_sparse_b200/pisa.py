@@ -476,6 +476,13 @@ def _at(t, dtype, n, dev):
     return t.data_ptr()
 
 
+def _token(t, dtype, n, dev):
+    """The address of a token's rows a sequence, [B, Hkv, d] or [B, Hkv, 1, d]."""
+    if t.dim() == 4 and t.shape[2] != 1:
+        raise ValueError(f"expected one row a sequence, got {t.shape[2]}")
+    return _at(t, dtype, n, dev)
+
+
 def _go(dev, fn, *args) -> None:
     """fn on device dev and its current stream."""
     if dev == torch._C._cuda_getDevice():
@@ -574,7 +581,7 @@ def pisa_paged_attn(cfg, pages, q, k_new, v_new, K, V, table, lens, o, lse, ws):
     rows, row = B * cfg.Hq, cfg.Hkv * d
     n = pages.P * S * row
     _go(dev, (_lib or load()).pisa_paged_attn, cfg, pages, _at(q, dt, rows * d, dev),
-        None if k_new is None else _at(k_new, dt, B * row, dev), None if v_new is None else _at(v_new, dt, B * row, dev),
+        None if k_new is None else _token(k_new, dt, B * row, dev), None if v_new is None else _token(v_new, dt, B * row, dev),
         _at(K, dt, n, dev), _at(V, dt, n, dev), _at(table, _i32, B * -(-cfg.N // S), dev), _at(lens, _i32, B, dev),
         _at(o, dt, rows * d, dev), None if lse is None else _at(lse, torch.float32, rows, dev),
         _at(ws, torch.uint8, 0, dev), ws.numel())
@@ -592,7 +599,7 @@ def pisa_paged_pyramid_append(cfg, pages, k_new, v_new, K, V, table, lens, pyr):
     """One token's rows into the pages (token lens[b] - 1) and into the summaries."""
     dev, dt, B, S, row = _dev(K), _elem(cfg), cfg.B, pages.S, cfg.Hkv * cfg.d
     n = pages.P * S * row
-    _go(dev, (_lib or load()).pisa_paged_pyramid_append, cfg, pages, _at(k_new, dt, B * row, dev), _at(v_new, dt, B * row, dev),
+    _go(dev, (_lib or load()).pisa_paged_pyramid_append, cfg, pages, _token(k_new, dt, B * row, dev), _token(v_new, dt, B * row, dev),
         _at(K, dt, n, dev), _at(V, dt, n, dev), _at(table, _i32, B * -(-cfg.N // S), dev), _at(lens, _i32, B, dev),
         _at(pyr, torch.float32, B * row * pisa_pyramid_rows(cfg), dev))
 
@@ -603,8 +610,8 @@ def pisa_paged_decode_step(cfg, pages, q_new, k_new, v_new, K, V, table, lens, p
     heads = cfg.Hkv
     row, qn = heads * d, B * cfg.Hq * d
     n = pages.P * S * row
-    _go(dev, (_lib or load()).pisa_paged_decode_step, cfg, pages, _at(q_new, dt, qn, dev), _at(k_new, dt, B * row, dev),
-        _at(v_new, dt, B * row, dev), _at(K, dt, n, dev), _at(V, dt, n, dev), _at(table, _i32, B * -(-cfg.N // S), dev),
+    _go(dev, (_lib or load()).pisa_paged_decode_step, cfg, pages, _at(q_new, dt, qn, dev), _token(k_new, dt, B * row, dev),
+        _token(v_new, dt, B * row, dev), _at(K, dt, n, dev), _at(V, dt, n, dev), _at(table, _i32, B * -(-cfg.N // S), dev),
         _at(lens, _i32, B, dev), _at(pyr, torch.float32, B * row * pisa_pyramid_rows(cfg), dev),
         _at(idx, _i32, B * heads * cfg.K, dev), _at(o, dt, qn, dev))
 
