@@ -22,11 +22,12 @@
 // starts sooner: the clusters use it).
 //
 // Bound by HBM: every byte is read once (16 sequences of 16 K tokens, 8 KV heads: 1.071 GB
-// of DRAM reads for 1.068 GB of keys and values; tensor pipe 10%, issue slots 27% busy).
-// 64 such sequences take 640 us, 256 K tokens of one 159 us (101% and 103% of a copy's
-// bandwidth, back to back). Both run at the board's power limit, so what took
-// instructions away made them faster: heads as the 8 columns of a product instead of its
-// 16 rows 729 -> 696 us, TMA instead of cp.async 696 -> 640.
+// of DRAM reads for 1.068 GB of keys and values; tensor pipe 15%, issue slots 31% busy).
+// 64 such sequences take 660 to 690 us, 256 K tokens of one 168 to 173 us, back to back (98
+// to 94% and 98 to 95% of a copy's bandwidth, by the GPU). Both run at the board's power
+// limit, so instructions cost time: heads as the 8 columns of a product instead of its 16
+// rows took 64 sequences from 729 to 696 us, TMA instead of cp.async to 640; all 24 bits of
+// the probabilities and rounded sums over tiles (pisa_tiles.cuh) added 3% and 1%.
 #include <cooperative_groups.h>
 #include <cuda.h>  // CUtensorMap
 
@@ -43,9 +44,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kStages = 3;
 constexpr int kStageBytes = 2 * kTileBytes;  // KT key rows, then KT value rows
-constexpr int kUnitCost = 1;  // 0: 104 us, 1: 77.6, 2: 78.9, 4: 83.1 for 64 sequences of 0..15 K tokens, 32 / 8 heads
-constexpr int kClusterTiles = 4;  // most tiles for a cluster's CTA (1 K tokens, 8 heads: 6.3 us, by the list 7.2 and a second
-                                  // launch; 4 K tokens, 32 units in fp32: 11.9, by the list 9.2)
+constexpr int kUnitCost = 1;  // 0: 103.5 us, 1: 80.1, 2: 81.1, 4: 83.9 for 64 sequences of 0..15 K tokens, 32 / 8 heads
+constexpr int kClusterTiles = 4;  // most tiles for a cluster's CTA (1 K tokens, 8 heads: 6.3 us, by the list 7.9 and a second
+                                  // launch; 2 K: 8.7 and 8.9; 4 K, with 8 tiles a CTA: 13.4, by the list 10.3)
 
 // rows [y, y + box) x 128 bytes from x (elements) of a pool into shared memory
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {

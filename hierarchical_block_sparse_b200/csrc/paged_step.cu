@@ -11,10 +11,10 @@
 // shared memory, G times for every element, and merges softmax states a tile at a
 // time: from G = 4 on that is what its time goes to. Here phases 2 and 4 cost 16
 // tensor-core products a 16 keys (fp32: the queries stay in registers) and the
-// softmax is taken once: 64 sequences of 12 to 16 K tokens, 8 heads: 139.8 -> 82.7 us (84%
-// of the HBM floor of 69.5); 8 heads a group at 665 tokens: 174 -> 35 us (fp32: 225 -> 62);
-// 16 a group at 8 K: 432 -> 62 us. What bounds it is the chain of dependent phases: about
-// 13 us of walk, one level after another, in which HBM is idle.
+// softmax is taken once (8 KV heads, decode.cu's kernel over pages against this one): 64
+// sequences of 16 K tokens 136 -> 83 us (84% of the HBM floor); 32 of 665 tokens with groups of
+// 8 178 -> 33 us (fp32: 239 -> 66); 8 of 32 K with groups of 16 422 -> 71 us. What bounds it is the
+// chain of dependent phases: about 13 us of walk, one level after another, in which HBM is idle.
 #include "pisa_decode.cuh"
 #include "pisa_paged.cuh"
 #include "pisa_tiles.cuh"
@@ -212,10 +212,10 @@ cudaError_t launch_shape(const void* q, const void* k_new, const void* v_new, vo
 }
 
 // Up to one unit an SM: 8 warps and a longer ring each, for a CTA has its SM alone (64 units
-// of 4 x 8 heads at 32 K tokens: 63 us with 4 warps, 42 with 8). Up to two: 8 warps where two such
-// CTAs fit (G <= 4; 256 units at 8 K tokens: 62 us with 4 warps, 50 with 8; with groups of 8, where
-// one fits, 35 and 44 at 665 tokens). More: 4 warps, 4 CTAs (512 units: 82.5 us; 93 with 8 warps,
-// 118 with rings of 3 stages, which let 3 CTAs share an SM).
+// at 32 K tokens: 45 us with 4 warps, 31 with 8; groups of 4: 53 and 38, of 16: 92 and 71). Up to two: 8
+// warps where two such CTAs fit (G <= 4; 256 units at 8 K tokens, groups of 4: 64 us with 4 warps, 52 with
+// 8; with groups of 8, where one fits, 75 and 90). More: 4 warps, 4 CTAs (512 units at 16 K tokens: 83 us;
+// 94 with 8 warps, 120 with rings of 3 stages, which let 3 CTAs share an SM).
 template <class Tile>
 cudaError_t launch_step(const void* q, const void* k_new, const void* v_new, void* K, void* V, const int32_t* len,
                         float* pyr, int32_t* idx, void* o, const PagedDecodeParams& p, cudaStream_t st, bool* taken) {
